@@ -20,6 +20,7 @@ STATUS_NAMES = {0: "ETP_OK", 1: "ETP_ERR_INVALID_ARG", 2: "ETP_ERR_IRREPS", 3: "
 
 # exported symbols and their C signatures (restype, argtypes)
 _vp, _i, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+_ll = ctypes.c_longlong
 _ip = ctypes.POINTER(ctypes.c_int)
 _dp = ctypes.POINTER(ctypes.c_double)
 
@@ -52,6 +53,12 @@ SIGNATURES = {
     "etp_node_ladder_full_step_floats": (_sz, [_i, _i]),
     "etp_node_ladder_full_workspace_bytes": (_sz, [_i, _i, _i]),
     "etp_node_ladder_full": (_i, [_i, _i, _i, _i, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "etp_checkpoint_store": (_i, [_i, _i, _ll, _i, _vp, _vp, _vp, _vp]),
+    "etp_checkpoint_restore": (_i, [_i, _i, _ll, _i, _vp, _vp, _vp, _vp]),
+    "etp_group_norm_workspace_bytes": (_sz, [_i, _i, _i, _i]),
+    "etp_group_norm": (_i, [_i, _i, _i, _i, _i, _vp, _i, _vp, _vp, _vp, _f, _i, _i, _vp, _vp, _i, _vp, _vp, _vp, _sz, _vp]),
+    "etp_group_norm_backward": (_i, [_i, _i, _i, _i, _i, _vp, _i, _vp, _i, _vp, _vp, _vp, _vp, _vp, _i, _vp, _i, _vp, _vp,
+                                     _vp, _vp, _sz, _vp]),
     "etp_forces": (_i, [_i, _i, _vp, _vp, _vp, _vp, _vp, _vp]),
     "etp_graph_workspace_bytes": (_sz, [_i, _i]),
     "etp_neighbors": (_i, [_vp, _i, _dp, _ip, _f, _i, _ip, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
@@ -259,6 +266,10 @@ class EdgeConv:
         stream = _stream(device) if device is not None else None
         _check(load_library().etp_get_status(self._h, stream, ctypes.byref(code)), "etp_get_status")
 
+    def _features(self, x):
+        """Node features as float32: a tensor's, or those that a Checkpoint8 holds."""
+        return x.restore(dtype=_torch().float32) if isinstance(x, Checkpoint8) else _f32(x)
+
     def _workspace(self, n_nodes, n_edges, device, workspace):
         torch = _torch()
         nb = self.workspace_bytes(n_nodes, n_edges)
@@ -289,9 +300,10 @@ class EdgeConv:
 
     def backward(self, graph, x, W, grad_out, want_grad_x=True, want_grad_vec=True, grad_x=None,
                  grad_vec=None, workspace=None, path_mask=None):
+        """x: the forward's node features, or their Checkpoint8."""
         torch = _torch()
-        _need_cuda(x, W, grad_out)
-        x, W, grad_out = _f32(x), _f32(W), _f32(grad_out)
+        _need_cuda(x.q if isinstance(x, Checkpoint8) else x, W, grad_out)
+        x, W, grad_out = self._features(x), _f32(W), _f32(grad_out)
         dev = x.device
         if want_grad_x and grad_x is None:
             grad_x = torch.empty((graph.n_nodes, self.info["dim_in"]), dtype=torch.float32, device=dev)
@@ -316,10 +328,10 @@ class EdgeConv:
 
     def backward_weights(self, graph, x, grad_out, grad_W=None, workspace=None):
         """dL/dW for L = <grad_out, forward(graph, x, W)>: [n_basis, n_paths, C], or [n_basis, cols] for
-        a general irreps handle."""
+        a general irreps handle. x: the forward's node features, or their Checkpoint8."""
         torch = _torch()
-        _need_cuda(x, grad_out)
-        x, grad_out = _f32(x), _f32(grad_out)
+        _need_cuda(x.q if isinstance(x, Checkpoint8) else x, grad_out)
+        x, grad_out = self._features(x), _f32(grad_out)
         if grad_W is None:
             shape = ((self.info["n_basis"], self.info["n_paths"], self.info["channels"]) if not self.info["general"]
                      else (self.info["n_basis"], self.info["weight_numel"] // self.info["n_basis"]))
@@ -391,9 +403,295 @@ def node_ladder_full(A, Ws, lmax, out=None, workspace=None):
     return out
 
 
-def edge_conv_function():
-    """torch.autograd.Function: out = conv(x, edge_vec, W); gradients for x, edge_vec and W."""
+# ---- between two convolutions: 8-bit checkpoints, group norm with an activation
+
+CKPT_FORMATS = {None: 0, "none": 0, "int8": 1, "e4m3": 2}
+ACTIVATIONS = {None: 0, "none": 0, "silu": 1}
+CKPT_BLOCK = 32   # values of a row that share a checkpoint scale
+_DTYPE_CODES = {}
+
+
+def _dtype_code(dtype):
+    if not _DTYPE_CODES:
+        torch = _torch()
+        _DTYPE_CODES.update({torch.float32: 0, torch.bfloat16: 1, torch.float16: 2})
+    code = _DTYPE_CODES.get(dtype)
+    if code is None:
+        raise ValueError(f"float32, bfloat16 or float16 values expected, got {dtype}")
+    return code
+
+
+def _named(table, name, what):
+    if name not in table:
+        raise ValueError(f"{what} must be one of {[k for k in table if k]} or None, got {name!r}")
+    return table[name]
+
+
+def _rows(t):
+    """t contiguous and 16-byte aligned (a copy where it is not)."""
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
+def _call(device, where, fn, *args):
+    """Calls a library function with the current stream of ``device``, which is made current for it."""
     torch = _torch()
+    if torch.cuda.current_device() == device.index:
+        st = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    if st != ETP_OK:
+        raise EtpError(st, where)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _same_device(x, *others):
+    _need_cuda(x, *others)
+    for t in others:
+        if t is not None and t.device != x.device:
+            raise ValueError(f"tensors on {x.device} and {t.device} in one call")
+
+
+@dataclass
+class Checkpoint8:
+    """Activations kept in 8 bits: 1 + 1/32 byte a value.
+
+    q: codes in the shape of the activations, int8 or float8_e4m3fn; scale: uint8 [..., ceil(cols / 32)],
+    32 values of a row share the scale 2^(byte - 127) (255: the run held a NaN or an infinity and
+    restores as NaN); dtype: type of the activations.
+    """
+    q: object
+    scale: object
+    dtype: object
+
+    @property
+    def shape(self):
+        return self.q.shape
+
+    @property
+    def format(self):
+        return "int8" if self.q.dtype == _torch().int8 else "e4m3"
+
+    @property
+    def nbytes(self):
+        return self.q.numel() + self.scale.numel()
+
+    def _checked(self):
+        torch = _torch()
+        _same_device(self.q, self.scale)
+        cols = self.q.shape[-1]
+        if self.q.dtype not in (torch.int8, torch.float8_e4m3fn) or self.scale.dtype != torch.uint8:
+            raise ValueError("a checkpoint has int8 or float8_e4m3fn codes and uint8 scales")
+        if self.scale.shape != self.q.shape[:-1] + (-(-cols // CKPT_BLOCK),):
+            raise ValueError(f"scales of shape {tuple(self.scale.shape)} do not fit codes of shape {tuple(self.q.shape)}")
+        return _rows(self.q), self.scale.contiguous()
+
+    def restore(self, dtype=None, out=None):
+        """The values the checkpoint stands for, in ``dtype`` (default: that of the activations)."""
+        torch = _torch()
+        q, scale = self._checked()
+        if out is None:
+            out = torch.empty(q.shape, dtype=dtype or self.dtype, device=q.device)
+        elif out.shape != q.shape or not out.is_contiguous() or (dtype is not None and out.dtype != dtype):
+            raise ValueError("out must be contiguous, of the checkpoint's shape and the dtype asked for")
+        _same_device(q, out)
+        cols = q.shape[-1]
+        _call(q.device, "etp_checkpoint_restore", load_library().etp_checkpoint_restore, CKPT_FORMATS[self.format],
+              _dtype_code(out.dtype), q.numel() // max(cols, 1), cols, q.data_ptr(), scale.data_ptr(), out.data_ptr())
+        return out
+
+
+def _empty_checkpoint(x, fmt):
+    torch = _torch()
+    return Checkpoint8(torch.empty(x.shape, dtype=torch.int8 if fmt == 1 else torch.float8_e4m3fn, device=x.device),
+                       torch.empty(x.shape[:-1] + (-(-x.shape[-1] // CKPT_BLOCK),), dtype=torch.uint8, device=x.device),
+                       x.dtype)
+
+
+def checkpoint8(x, fmt="int8"):
+    """8-bit checkpoint of x [..., cols] (float32, bfloat16 or float16 CUDA tensor): a Checkpoint8.
+
+    fmt "int8": values within half a step of max|x| / 63.5 of their run of 32 at most; "e4m3": within
+    2^-4 of each value, or 2^-10 of the scale. EdgeConv.backward, EdgeConv.backward_weights and
+    group_norm_backward take a Checkpoint8 in the place of x.
+    """
+    code = _named(CKPT_FORMATS, fmt, "fmt")
+    if code == 0:
+        raise ValueError("fmt must be 'int8' or 'e4m3'")
+    _need_cuda(x)
+    if x.dim() < 1:
+        raise ValueError("x needs at least one dimension")
+    dtype = _dtype_code(x.dtype)
+    x = x.contiguous()
+    ck = _empty_checkpoint(x, code)
+    cols = x.shape[-1]
+    _call(x.device, "etp_checkpoint_store", load_library().etp_checkpoint_store, code, dtype, x.numel() // max(cols, 1),
+          cols, x.data_ptr(), ck.q.data_ptr(), ck.scale.data_ptr())
+    return ck
+
+
+def group_norm_workspace_bytes(lmax, channels, groups, backward=False):
+    return int(load_library().etp_group_norm_workspace_bytes(int(lmax), int(channels), int(groups), int(backward)))
+
+
+def _norm_shape(shape, lmax, groups, node_ptr, weight, bias):
+    """(rows, channels, structures) of the checked arguments."""
+    if len(shape) != 2:
+        raise ValueError("node rows are [n_nodes, channels (lmax + 1)^2]")
+    n, dim = shape
+    comps = (lmax + 1) ** 2
+    if lmax < 0 or dim % comps or dim == 0:
+        raise ValueError(f"rows of {dim} values do not hold (lmax + 1)^2 = {comps} components")
+    c = dim // comps
+    if node_ptr is not None and (node_ptr.dim() != 1 or node_ptr.numel() < 1):
+        raise ValueError("node_ptr is a vector of n_structs + 1 row numbers")
+    if weight is not None and tuple(weight.shape) != (lmax + 1, c):
+        raise ValueError(f"weight must be [{lmax + 1}, {c}], got {tuple(weight.shape)}")
+    if bias is not None and tuple(bias.shape) != (c,):
+        raise ValueError(f"bias must be [{c}], got {tuple(bias.shape)}")
+    return n, c, 1 if node_ptr is None else node_ptr.numel() - 1
+
+
+def _norm_workspace(lmax, c, groups, backward, device, workspace):
+    nb = group_norm_workspace_bytes(lmax, c, groups, backward)
+    if workspace is None or workspace.numel() < nb:
+        workspace = _torch().empty(max(nb, 1), dtype=_torch().uint8, device=device)
+    return workspace, nb
+
+
+def _into(out, shape, dtype, device, what):
+    """(tensor to write, whether the library made it)"""
+    if out is None:
+        return _torch().empty(shape, dtype=dtype, device=device), True
+    if tuple(out.shape) != tuple(shape) or out.dtype != dtype or out.device != device or not out.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+    return out, False
+
+
+def group_norm(x, weight, bias, lmax, groups, node_ptr=None, eps=1e-5, activation="silu", checkpoint=None, out=None,
+               stats=None, workspace=None):
+    """Group norm with an activation on node rows: (out, stats, checkpoint).
+
+    x: [N, C (lmax+1)^2] CUDA tensor in the uniform node-row layout (float32, bfloat16, float16);
+    weight [lmax+1, C], bias [C] (float32, or None); node_ptr: int32 [S + 1] starts of the structures'
+    rows (None: one structure). Statistics per structure, rank and group of C / groups channels: mean and
+    variance for l = 0, mean square for l > 0. activation "silu": SiLU on l = 0, the same channel's
+    logistic gate on l > 0. stats: [S, lmax + 2, groups] (mean; 1 / deviation of every rank), for the
+    backward. checkpoint "int8" or "e4m3": also returns the Checkpoint8 of x (else None), in the same
+    pass when C % 32 == 0. Rows of no structure: untouched in a given ``out``, zero in a new one.
+    """
+    torch = _torch()
+    _same_device(x, weight, bias, node_ptr)
+    dtype = _dtype_code(x.dtype)
+    n, c, s = _norm_shape(x.shape, lmax, groups, node_ptr, weight, bias)
+    act, fmt = _named(ACTIVATIONS, activation, "activation"), _named(CKPT_FORMATS, checkpoint, "checkpoint")
+    x = _rows(x)
+    dev = x.device
+    weight = None if weight is None else _f32(weight)
+    bias = None if bias is None else _f32(bias)
+    node_ptr = None if node_ptr is None else _i32(node_ptr)
+    out, made = _into(out, x.shape, x.dtype, dev, "out")
+    stats, _ = _into(stats, (s, lmax + 2, groups), torch.float32, dev, "stats")
+    ck = _empty_checkpoint(x, fmt) if fmt else None
+    ws, nb = _norm_workspace(lmax, c, groups, False, dev, workspace)
+    _call(dev, "etp_group_norm", load_library().etp_group_norm, lmax, c, groups, n, s, _addr(node_ptr), dtype,
+          x.data_ptr(), _addr(weight), _addr(bias), eps, act, int(made), out.data_ptr(), stats.data_ptr(), fmt,
+          ck.q.data_ptr() if ck else None, ck.scale.data_ptr() if ck else None, ws.data_ptr(), nb)
+    return out, stats, ck
+
+
+def group_norm_backward(x, stats, weight, bias, grad_out, lmax, groups, node_ptr=None, activation="silu",
+                        want_grad_x=True, want_grad_affine=True, grad_x=None, workspace=None):
+    """(grad_x, grad_weight, grad_bias) for the cotangent grad_out of group_norm's out.
+
+    x: group_norm's input or its Checkpoint8, whose codes are read directly; stats: from group_norm.
+    grad_weight [lmax+1, C] and grad_bias [C] are float32 sums over all structures (None when
+    want_grad_affine is false). Rows of no structure: untouched in a given ``grad_x``, zero in a new one.
+    """
+    torch = _torch()
+    kept = isinstance(x, Checkpoint8)
+    _same_device(grad_out, x.q if kept else x, stats, weight, bias, node_ptr)
+    dtype = _dtype_code(grad_out.dtype)
+    n, c, s = _norm_shape(x.shape, lmax, groups, node_ptr, weight, bias)
+    act = _named(ACTIVATIONS, activation, "activation")
+    if grad_out.shape != x.shape or (not kept and grad_out.dtype != x.dtype):
+        raise ValueError(f"grad_out must have x's shape and type, got {tuple(grad_out.shape)} {grad_out.dtype}")
+    if tuple(stats.shape) != (s, lmax + 2, groups):
+        raise ValueError(f"stats must be [{s}, {lmax + 2}, {groups}], got {tuple(stats.shape)}")
+    if not (want_grad_x or want_grad_affine):
+        return None, None, None
+    dev = grad_out.device
+    grad_out, stats = _rows(grad_out), _f32(stats)
+    q = scale = None
+    if kept:
+        q, scale = x._checked()
+    else:
+        x = _rows(x)
+    weight = None if weight is None else _f32(weight)
+    bias = None if bias is None else _f32(bias)
+    node_ptr = None if node_ptr is None else _i32(node_ptr)
+    made = False
+    if want_grad_x:
+        grad_x, made = _into(grad_x, grad_out.shape, grad_out.dtype, dev, "grad_x")
+    gw = torch.empty((lmax + 1, c), dtype=torch.float32, device=dev) if want_grad_affine else None
+    gb = torch.empty(c, dtype=torch.float32, device=dev) if want_grad_affine else None
+    ws, nb = _norm_workspace(lmax, c, groups, True, dev, workspace)
+    _call(dev, "etp_group_norm_backward", load_library().etp_group_norm_backward, lmax, c, groups, n, s, _addr(node_ptr),
+          dtype, None if kept else x.data_ptr(), CKPT_FORMATS[x.format] if kept else 0, _addr(q), _addr(scale),
+          stats.data_ptr(), _addr(weight), _addr(bias), act, grad_out.data_ptr(), int(made),
+          grad_x.data_ptr() if want_grad_x else None, _addr(gw), _addr(gb), ws.data_ptr(), nb)
+    return (grad_x if want_grad_x else None), gw, gb
+
+
+def group_norm_function(checkpoint=None):
+    """torch.autograd.Function: out = group_norm(x, weight, bias, lmax, groups, node_ptr, eps, activation);
+    gradients for x, weight and bias. checkpoint "int8" or "e4m3": the input is kept for the backward in
+    8 bits, and the gradients are taken at the kept values.
+    """
+    torch = _torch()
+    _named(CKPT_FORMATS, checkpoint, "checkpoint")
+
+    class _GroupNormFn(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, weight, bias, lmax, groups, node_ptr=None, eps=1e-5, activation="silu"):
+            out, stats, ck = group_norm(x.detach(), None if weight is None else weight.detach(),
+                                        None if bias is None else bias.detach(), lmax, groups, node_ptr, eps, activation,
+                                        checkpoint)
+            ctx.args = (lmax, groups, node_ptr, activation)
+            ctx.kept_dtype = ck.dtype if ck else None
+            ctx.save_for_backward(*((ck.q, ck.scale) if ck else (x, None)), stats, weight, bias)
+            return out
+
+        @staticmethod
+        @torch.autograd.function.once_differentiable
+        def backward(ctx, grad_out):
+            x, scale, stats, weight, bias = ctx.saved_tensors
+            if ctx.kept_dtype is not None:
+                x = Checkpoint8(x, scale, ctx.kept_dtype)
+            lmax, groups, node_ptr, activation = ctx.args
+            need = ctx.needs_input_grad
+            gx, gw, gb = group_norm_backward(x, stats, weight, bias, grad_out, lmax, groups, node_ptr, activation,
+                                             need[0], need[1] or need[2])
+            return (gx, gw.to(weight.dtype) if need[1] else None, gb.to(bias.dtype) if need[2] else None, None, None,
+                    None, None, None)
+
+    return _GroupNormFn
+
+
+def edge_conv_function(checkpoint=None):
+    """torch.autograd.Function: out = conv(x, edge_vec, W); gradients for x, edge_vec and W.
+
+    checkpoint "int8" or "e4m3": the node features are kept for the backward in 8 bits instead of
+    float32; the gradients for edge_vec and W are taken at the kept values (that for x does not depend
+    on x).
+    """
+    torch = _torch()
+    _named(CKPT_FORMATS, checkpoint, "checkpoint")
+    keep = CKPT_FORMATS[checkpoint] != 0
 
     class _EdgeConvFn(torch.autograd.Function):
         @staticmethod
@@ -401,12 +699,21 @@ def edge_conv_function():
             g = Graph(graph.n_nodes, graph.n_edges, graph.row_ptr, graph.sender, edge_vec.detach(),
                       graph.t_row_ptr, graph.t_perm)
             ctx.conv, ctx.graph = conv, g
-            ctx.save_for_backward(x, W)
+            if keep:
+                ck = checkpoint8(x.detach(), checkpoint)
+                ctx.kept_dtype = ck.dtype
+                ctx.save_for_backward(ck.q, ck.scale, W)
+            else:
+                ctx.save_for_backward(x, W)
             return conv.forward(g, x.detach(), W.detach())
 
         @staticmethod
         def backward(ctx, grad_out):
-            x, W = ctx.saved_tensors
+            if keep:
+                q, scale, W = ctx.saved_tensors
+                x = Checkpoint8(q, scale, ctx.kept_dtype).restore(dtype=torch.float32)
+            else:
+                x, W = ctx.saved_tensors
             go = grad_out.contiguous()
             gx = gv = gW = None
             if ctx.needs_input_grad[2] or ctx.needs_input_grad[3]:

@@ -8,6 +8,7 @@
 #include <vector>
 
 #include "etp_internal.h"
+#include "etp_norm.h"
 #include "generated/etp_paths.h"
 
 struct etp_ctx {
@@ -823,6 +824,144 @@ etp_status etp_node_ladder_full(int lmax, int channels, int n_nodes, int nu, con
     return ETP_ERR_CUDA;
   }
   return ETP_OK;
+}
+
+static bool known(etp_dtype t) { return t == ETP_F32 || t == ETP_BF16 || t == ETP_F16; }
+
+static etp_status check_checkpoint(const char* who, etp_ckpt_format format, etp_dtype dtype, long long rows, int cols,
+                                   const void* x, const void* q, const void* scale) {
+  if ((format != ETP_CKPT_INT8 && format != ETP_CKPT_E4M3) || !known(dtype)) {
+    set_error(std::string(who) + ": unknown format or dtype");
+    return ETP_ERR_INVALID_ARG;
+  }
+  if (rows < 0 || cols < 0) {
+    set_error(std::string(who) + ": negative size");
+    return ETP_ERR_INVALID_ARG;
+  }
+  if (cols > 0 && rows >= (1LL << 40) / cols) {
+    set_error(std::string(who) + ": rows * cols must stay below 2^40");
+    return ETP_ERR_UNSUPPORTED;
+  }
+  if (rows > 0 && cols > 0 && (!x || !q || !scale)) {
+    set_error(std::string(who) + ": NULL array");
+    return ETP_ERR_INVALID_ARG;
+  }
+  if (reinterpret_cast<uintptr_t>(x) % (dtype == ETP_F32 ? 4 : 2) != 0) {
+    set_error(std::string(who) + ": x must be aligned to its values");
+    return ETP_ERR_INVALID_ARG;
+  }
+  return ETP_OK;
+}
+
+etp_status etp_checkpoint_store(etp_ckpt_format format, etp_dtype dtype, long long rows, int cols, const void* x,
+                                void* q, void* scale, void* stream) {
+  etp_status st = check_checkpoint("etp_checkpoint_store", format, dtype, rows, cols, x, q, scale);
+  if (st != ETP_OK || rows == 0 || cols == 0) return st;
+  return ckpt::store(format, dtype, rows, cols, x, static_cast<uint8_t*>(q), static_cast<uint8_t*>(scale),
+                     static_cast<cudaStream_t>(stream));
+}
+
+etp_status etp_checkpoint_restore(etp_ckpt_format format, etp_dtype dtype, long long rows, int cols, const void* q,
+                                  const void* scale, void* x, void* stream) {
+  etp_status st = check_checkpoint("etp_checkpoint_restore", format, dtype, rows, cols, x, q, scale);
+  if (st != ETP_OK || rows == 0 || cols == 0) return st;
+  return ckpt::restore(format, dtype, rows, cols, static_cast<const uint8_t*>(q), static_cast<const uint8_t*>(scale), x,
+                       static_cast<cudaStream_t>(stream));
+}
+
+size_t etp_group_norm_workspace_bytes(int lmax, int channels, int groups, int backward) {
+  if (!norm::supported(lmax, channels, groups)) return 0;
+  norm::Call c{};
+  c.lmax = lmax;
+  c.channels = channels;
+  c.groups = groups;
+  return norm::workspace_bytes(c, backward != 0);
+}
+
+// The checks that both directions of the group norm share.
+static etp_status check_norm(const char* who, const norm::Call& c, etp_ckpt_format format, bool backward,
+                             const void* workspace, size_t workspace_bytes) {
+  if (!norm::supported(c.lmax, c.channels, c.groups)) {
+    set_error(std::string(who) + ": lmax 0..3; groups <= 64 must divide channels; channels <= 256, or <= 1024 when "
+              "channels and channels / groups are multiples of 4");
+    return ETP_ERR_UNSUPPORTED;
+  }
+  if (!known(c.dtype) || (c.activation != ETP_ACT_NONE && c.activation != ETP_ACT_SILU) ||
+      (format != ETP_CKPT_NONE && format != ETP_CKPT_INT8 && format != ETP_CKPT_E4M3)) {
+    set_error(std::string(who) + ": unknown dtype, activation or checkpoint format");
+    return ETP_ERR_INVALID_ARG;
+  }
+  if (c.n_nodes < 0 || c.n_structs < 0) {
+    set_error(std::string(who) + ": negative size");
+    return ETP_ERR_INVALID_ARG;
+  }
+  if (!c.node_ptr && c.n_structs != 1) {
+    set_error(std::string(who) + ": node_ptr may be NULL only with n_structs = 1");
+    return ETP_ERR_INVALID_ARG;
+  }
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
+      workspace_bytes < norm::workspace_bytes(c, backward)) {
+    set_error(std::string(who) + ": workspace missing, misaligned or smaller than etp_group_norm_workspace_bytes()");
+    return ETP_ERR_INVALID_ARG;
+  }
+  return ETP_OK;
+}
+
+etp_status etp_group_norm(int lmax, int channels, int groups, int n_nodes, int n_structs, const int* node_ptr,
+                          etp_dtype dtype, const void* x, const float* weight, const float* bias, float eps,
+                          etp_activation activation, int zero_rest, void* out, float* stats, etp_ckpt_format format,
+                          void* q, void* scale, void* workspace, size_t workspace_bytes, void* stream) {
+  const char* who = "etp_group_norm";
+  const norm::Call c{lmax, channels, groups, n_nodes, n_structs, node_ptr, dtype, activation, zero_rest};
+  etp_status st = check_norm(who, c, format, false, workspace, workspace_bytes);
+  if (st != ETP_OK) return st;
+  if (!(eps >= 0.0f) || (n_structs > 0 && !stats) ||
+      (n_nodes > 0 && (!x || !out || (format != ETP_CKPT_NONE && (!q || !scale))))) {
+    set_error(std::string(who) + ": NULL array or negative eps");
+    return ETP_ERR_INVALID_ARG;
+  }
+  if (!aligned16(x) || !aligned16(out) || reinterpret_cast<uintptr_t>(q) % 4 != 0) {
+    set_error(std::string(who) + ": x and out must be 16-byte aligned, q 4-byte aligned");
+    return ETP_ERR_INVALID_ARG;
+  }
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (n_nodes == 0)
+    return n_structs == 0 ? ETP_OK
+                          : cuda_status(cudaMemsetAsync(stats, 0, sizeof(float) * n_structs * (lmax + 2) * groups, s), who);
+  if (validate_requested() && (st = norm::validate(c, workspace, s)) != ETP_OK) return st;
+  return norm::forward(c, x, weight, bias, eps, out, stats, format, static_cast<uint8_t*>(q),
+                       static_cast<uint8_t*>(scale), workspace, s);
+}
+
+etp_status etp_group_norm_backward(int lmax, int channels, int groups, int n_nodes, int n_structs,
+                                   const int* node_ptr, etp_dtype dtype, const void* x, etp_ckpt_format format,
+                                   const void* q, const void* scale, const float* stats, const float* weight,
+                                   const float* bias, etp_activation activation, const void* grad_out, int zero_rest,
+                                   void* grad_x, float* grad_weight, float* grad_bias, void* workspace,
+                                   size_t workspace_bytes, void* stream) {
+  const char* who = "etp_group_norm_backward";
+  const norm::Call c{lmax, channels, groups, n_nodes, n_structs, node_ptr, dtype, activation, zero_rest};
+  etp_status st = check_norm(who, c, format, true, workspace, workspace_bytes);
+  if (st != ETP_OK) return st;
+  if ((!grad_x && !grad_weight && !grad_bias) || (n_structs > 0 && !stats) ||
+      (n_nodes > 0 && (!grad_out || (format == ETP_CKPT_NONE ? !x : (!q || !scale))))) {
+    set_error(std::string(who) + ": NULL array, or no gradient asked for");
+    return ETP_ERR_INVALID_ARG;
+  }
+  if ((format == ETP_CKPT_NONE && !aligned16(x)) || !aligned16(grad_out) || !aligned16(grad_x) ||
+      (format != ETP_CKPT_NONE && reinterpret_cast<uintptr_t>(q) % 4 != 0)) {
+    set_error(std::string(who) + ": x, grad_out and grad_x must be 16-byte aligned, q 4-byte aligned");
+    return ETP_ERR_INVALID_ARG;
+  }
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (n_nodes == 0) {
+    cudaError_t e = grad_weight ? cudaMemsetAsync(grad_weight, 0, sizeof(float) * (lmax + 1) * channels, s) : cudaSuccess;
+    if (e == cudaSuccess && grad_bias) e = cudaMemsetAsync(grad_bias, 0, sizeof(float) * channels, s);
+    return cuda_status(e, who);
+  }
+  if (validate_requested() && (st = norm::validate(c, workspace, s)) != ETP_OK) return st;
+  return norm::backward(c, x, format, static_cast<const uint8_t*>(q), static_cast<const uint8_t*>(scale), stats, weight,
+                        bias, grad_out, grad_x, grad_weight, grad_bias, workspace, s);
 }
 
 etp_status etp_radial_weights(etp_handle h, int n_edges, const float* edge_vec, const float* W,

@@ -185,6 +185,14 @@ etp_status launch_general_backward(const GenParams& g, int n_nodes, int n_edges,
 etp_status launch_node_ladder(int lmax, int channels, int n_nodes, int nu, const float* A, const float* W,
                               float* out, cudaStream_t s);
 
+// ---- 8-bit checkpoints (etp_checkpoint.cu); group norm: etp_norm.h
+namespace ckpt {
+etp_status store(etp_ckpt_format format, etp_dtype dtype, long long rows, int cols, const void* x, uint8_t* q,
+                 uint8_t* scale, cudaStream_t s);
+etp_status restore(etp_ckpt_format format, etp_dtype dtype, long long rows, int cols, const uint8_t* q,
+                   const uint8_t* scale, void* x, cudaStream_t s);
+}  // namespace ckpt
+
 // ---- graph kernels (etp_graph.cu)
 size_t graph_workspace_bytes(int n_nodes, int max_edges);
 etp_status neighbors(const float* pos, int n_nodes, const double* cell, const int* pbc,

@@ -77,6 +77,15 @@ typedef enum {
   ETP_ERR_CAPACITY = 6       /* an output buffer or fixed scratch is smaller than needed (n_edges reported) */
 } etp_status;
 
+/* Value types of the calls that take more than float32 (etp_checkpoint_*, etp_group_norm*). */
+typedef enum { ETP_F32 = 0, ETP_BF16 = 1, ETP_F16 = 2 } etp_dtype;
+
+/* 8-bit checkpoint formats; ETP_CKPT_NONE: no checkpoint. */
+typedef enum { ETP_CKPT_NONE = 0, ETP_CKPT_INT8 = 1, ETP_CKPT_E4M3 = 2 } etp_ckpt_format;
+
+/* Activations of etp_group_norm. */
+typedef enum { ETP_ACT_NONE = 0, ETP_ACT_SILU = 1 } etp_activation;
+
 typedef struct {
   int lmax;          /* L: irreps_in = irreps_out = C x (0e + 1o + ... ), SH lmax = L */
   int channels;      /* C */
@@ -275,6 +284,65 @@ etp_status etp_radial_weights(etp_handle h, int n_edges, const float* edge_vec, 
  * summed in canonical (row) order and transposed (t_perm) order respectively. */
 etp_status etp_forces(int n_nodes, int n_edges, const int* row_ptr, const int* t_row_ptr,
                       const int* t_perm, const float* grad_edge_vec, float* forces, void* stream);
+
+/* ---- between two convolutions: 8-bit activation checkpoints, group norm with an activation ----
+ * For training: the backward of a convolution or of the norm needs that layer's input; kept in 8
+ * bits it takes 1 + 1/32 byte a value. */
+
+/* Checkpoint of x[rows][cols]: q[rows][cols] (bytes) and scale[rows][ceil(cols / 32)] (bytes). Each
+ * run of 32 values of a row (the last run of a row may be shorter) shares the scale 2^e, e the
+ * smallest integer >= -126 with max|x| <= 127 2^e (ETP_CKPT_INT8) or 448 2^e (ETP_CKPT_E4M3); q is
+ * x / 2^e rounded to the nearest integer or e4m3 number, ties to even; the scale byte is e + 127.
+ * A run with a NaN or an infinity gets scale byte 255 and codes 0. x: dtype values, aligned to their
+ * size; q is faster when 4-byte aligned with x 16-byte aligned. Device pointers; asynchronous. */
+etp_status etp_checkpoint_store(etp_ckpt_format format, etp_dtype dtype, long long rows, int cols, const void* x,
+                                void* q, void* scale, void* stream);
+
+/* x[rows][cols] = the values a checkpoint stands for, code 2^(scale - 127): exact in 32 bits, held to
+ * the largest finite value of dtype; NaN throughout a run whose scale byte is 255. */
+etp_status etp_checkpoint_restore(etp_ckpt_format format, etp_dtype dtype, long long rows, int cols, const void* q,
+                                  const void* scale, void* x, void* stream);
+
+/* Workspace of etp_group_norm (backward = 0) or etp_group_norm_backward (1) for any number of nodes
+ * and structures; 0 for shapes that are not supported. */
+size_t etp_group_norm_workspace_bytes(int lmax, int channels, int groups, int backward);
+
+/* Group norm with an activation on node rows x[n_nodes][dim], dim = channels (lmax + 1)^2, in the
+ * uniform layout. Structure s is the rows node_ptr[s] .. node_ptr[s+1] - 1 (node_ptr: [n_structs + 1]
+ * device ints, ascending, within [0, n_nodes]; NULL with n_structs = 1: all rows); group g is the
+ * channels g channels/groups .. For every structure s and group g, over the structure's rows, the
+ * group's channels u and the components m of a rank:
+ *   mu = mean x[., 0, u];  r_0 = 1 / sqrt(mean (x[., 0, u] - mu)^2 + eps);
+ *   r_l = 1 / sqrt(mean x[., l m, u]^2 + eps) for l > 0 (no mean: the norm commutes with rotations)
+ *   y_0 = (x_0 - mu) r_0 weight[0][u] + bias[u];  y_lm = x_lm r_l weight[l][u]
+ *   out_lm = y_lm (ETP_ACT_NONE) or y_lm / (1 + exp(-y_0)) (ETP_ACT_SILU: SiLU on l = 0, and the
+ *   same channel's scalar as the gate of l > 0).
+ * weight[lmax + 1][channels], bias[channels]: float32, NULL = ones / zeros. x, out: dtype values,
+ * 16-byte aligned; out may not overlap x. stats[n_structs][lmax + 2][groups] (float32) receives mu,
+ * r_0 .. r_lmax; zeros for a structure without rows. Rows that belong to no structure are left as
+ * they were in out, or zeroed if zero_rest is nonzero. format: ETP_CKPT_NONE, or the checkpoint of all
+ * rows of x is stored to q and scale as by etp_checkpoint_store (q 4-byte aligned), in the same pass
+ * when channels % 32 == 0. lmax 0..3; channels / groups whole, groups <= 64, channels <= 256, or
+ * <= 1024 when channels and channels / groups are multiples of 4; eps >= 0. Sums are 64-bit; equal
+ * calls give equal bits. Asynchronous (a cooperative launch); concurrent calls need their own
+ * workspace, 256-byte aligned. With ETP_VALIDATE=1 node_ptr is checked first (ETP_ERR_BAD_GRAPH; the
+ * stream is synchronised). */
+etp_status etp_group_norm(int lmax, int channels, int groups, int n_nodes, int n_structs, const int* node_ptr,
+                          etp_dtype dtype, const void* x, const float* weight, const float* bias, float eps,
+                          etp_activation activation, int zero_rest, void* out, float* stats, etp_ckpt_format format,
+                          void* q, void* scale, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Vector-Jacobian product of etp_group_norm for the cotangent grad_out (dtype): grad_x (dtype), and
+ * grad_weight[lmax + 1][channels], grad_bias[channels] (float32, sums over all structures). Any may be
+ * NULL, not all three. stats: from the forward. format ETP_CKPT_NONE: x is the forward's input;
+ * otherwise x is ignored and the input is read from its checkpoint q, scale. Rows of no structure add
+ * nothing; zero_rest as above, for grad_x. grad_x may not overlap grad_out or x. */
+etp_status etp_group_norm_backward(int lmax, int channels, int groups, int n_nodes, int n_structs,
+                                   const int* node_ptr, etp_dtype dtype, const void* x, etp_ckpt_format format,
+                                   const void* q, const void* scale, const float* stats, const float* weight,
+                                   const float* bias, etp_activation activation, const void* grad_out, int zero_rest,
+                                   void* grad_x, float* grad_weight, float* grad_bias, void* workspace,
+                                   size_t workspace_bytes, void* stream);
 
 /* ---- graph construction (integer outputs are bit-exact against a float64 brute force) ----
  * Defined by the pages' force workloads, which build the neighbour graph of periodic cells with
