@@ -203,7 +203,10 @@ def _norm_inputs(n, lmax, c, dtype, seed, offset=0.0):
     return x, w, b, g
 
 
-def _within(got, want, bound, what):
+def _within(got, want, bound, what, most=np.inf):
+    # a value that reaches past the type's largest finite one (`most`, and half a step) is infinite there
+    past = np.isinf(got) & (np.sign(got) == np.sign(want)) & (np.abs(want) + bound >= most * (1 + 2.0 ** -12))
+    got = np.where(past, want, got)
     off = np.abs(got - want) - bound
     assert np.isfinite(got).all() and off.max() <= 0, (what, float(np.abs(got - want).max()), float(off.max()))
 
@@ -257,7 +260,7 @@ def test_norm_backward(n, lmax, c, groups, kind, dtype, keep):
     bounds = norm_bounds(xin, w, b, lmax, groups, ptr, act, st, info.eps if dtype != "float32" else 0, grad=_np(g),
                          tiny=info.smallest_normal)
     for a, e, t, what in zip(got, want, bounds, ("grad_x", "grad_weight", "grad_bias")):
-        _within(_np(a), e, t + 1e-30, what)
+        _within(_np(a), e, t + 1e-30, what, info.max if dtype == "float16" and what == "grad_x" else np.inf)
     again = etp.group_norm_backward(ck if keep else xd, stats, wd, bd, g.to(DEV), lmax, groups, node_ptr, act)
     assert all(torch.equal(p, q) for p, q in zip(got, again))
 
@@ -517,12 +520,12 @@ def test_training_block(keep):
             d /= d.norm()
             h = 2e-2
             at = [[p.detach() + (s * h * d if p is t else 0) for p in leaves] for s in (1, -1)]
-            up, down = (float((run(*a).double() * go.double()).sum()) for a in at)
+            up, down = (float((run(*a).detach().double() * go.double()).sum()) for a in at)
             slope = float((grad.double() * d.double()).sum())
             scale = float(grad.double().norm())
             # truncation: h^2 / 6 of the third derivative, whose size is of the gradient's order; rounding:
             # 2^-24 of each of the sum's terms over h
-            size = float((run(*leaves).double() * go.double()).abs().sum())
+            size = float((run(*leaves).detach().double() * go.double()).abs().sum())
             assert abs((up - down) / (2 * h) - slope) <= 10 * h * h * scale + 40 * 2.0 ** -24 * size / h
 
 
