@@ -55,7 +55,7 @@ SIGNATURES = {
     "etp_node_ladder_full": (_i, [_i, _i, _i, _i, _vp, _vp, _vp, _vp, _sz, _vp]),
     "etp_checkpoint_store": (_i, [_i, _i, _ll, _i, _vp, _vp, _vp, _vp]),
     "etp_checkpoint_restore": (_i, [_i, _i, _ll, _i, _vp, _vp, _vp, _vp]),
-    "etp_group_norm_workspace_bytes": (_sz, [_i, _i, _i, _i]),
+    "etp_group_norm_workspace_bytes": (_sz, [_i, _i, _i, _i, _i]),
     "etp_group_norm": (_i, [_i, _i, _i, _i, _i, _vp, _i, _vp, _vp, _vp, _f, _i, _i, _vp, _vp, _i, _vp, _vp, _vp, _sz, _vp]),
     "etp_group_norm_backward": (_i, [_i, _i, _i, _i, _i, _vp, _i, _vp, _i, _vp, _vp, _vp, _vp, _vp, _i, _vp, _i, _vp, _vp,
                                      _vp, _vp, _sz, _vp]),
@@ -488,7 +488,7 @@ class Checkpoint8:
             raise ValueError("a checkpoint has int8 or float8_e4m3fn codes and uint8 scales")
         if self.scale.shape != self.q.shape[:-1] + (-(-cols // CKPT_BLOCK),):
             raise ValueError(f"scales of shape {tuple(self.scale.shape)} do not fit codes of shape {tuple(self.q.shape)}")
-        return _rows(self.q), self.scale.contiguous()
+        return _rows(self.q), _rows(self.scale)
 
     def restore(self, dtype=None, out=None):
         """The values the checkpoint stands for, in ``dtype`` (default: that of the activations)."""
@@ -534,8 +534,8 @@ def checkpoint8(x, fmt="int8"):
     return ck
 
 
-def group_norm_workspace_bytes(lmax, channels, groups, backward=False):
-    return int(load_library().etp_group_norm_workspace_bytes(int(lmax), int(channels), int(groups), int(backward)))
+def group_norm_workspace_bytes(lmax, channels, groups, n_structs=1, backward=False):
+    return load_library().etp_group_norm_workspace_bytes(int(lmax), int(channels), int(groups), int(n_structs), int(backward))
 
 
 def _norm_shape(shape, lmax, groups, node_ptr, weight, bias):
@@ -556,8 +556,8 @@ def _norm_shape(shape, lmax, groups, node_ptr, weight, bias):
     return n, c, 1 if node_ptr is None else node_ptr.numel() - 1
 
 
-def _norm_workspace(lmax, c, groups, backward, device, workspace):
-    nb = group_norm_workspace_bytes(lmax, c, groups, backward)
+def _norm_workspace(lmax, c, groups, s, backward, device, workspace):
+    nb = group_norm_workspace_bytes(lmax, c, groups, s, backward)
     if workspace is None or workspace.numel() < nb:
         workspace = _torch().empty(max(nb, 1), dtype=_torch().uint8, device=device)
     return workspace, nb
@@ -597,7 +597,7 @@ def group_norm(x, weight, bias, lmax, groups, node_ptr=None, eps=1e-5, activatio
     out, made = _into(out, x.shape, x.dtype, dev, "out")
     stats, _ = _into(stats, (s, lmax + 2, groups), torch.float32, dev, "stats")
     ck = _empty_checkpoint(x, fmt) if fmt else None
-    ws, nb = _norm_workspace(lmax, c, groups, False, dev, workspace)
+    ws, nb = _norm_workspace(lmax, c, groups, s, False, dev, workspace)
     _call(dev, "etp_group_norm", load_library().etp_group_norm, lmax, c, groups, n, s, _addr(node_ptr), dtype,
           x.data_ptr(), _addr(weight), _addr(bias), eps, act, int(made), out.data_ptr(), stats.data_ptr(), fmt,
           ck.q.data_ptr() if ck else None, ck.scale.data_ptr() if ck else None, ws.data_ptr(), nb)
@@ -639,7 +639,7 @@ def group_norm_backward(x, stats, weight, bias, grad_out, lmax, groups, node_ptr
         grad_x, made = _into(grad_x, grad_out.shape, grad_out.dtype, dev, "grad_x")
     gw = torch.empty((lmax + 1, c), dtype=torch.float32, device=dev) if want_grad_affine else None
     gb = torch.empty(c, dtype=torch.float32, device=dev) if want_grad_affine else None
-    ws, nb = _norm_workspace(lmax, c, groups, True, dev, workspace)
+    ws, nb = _norm_workspace(lmax, c, groups, s, True, dev, workspace)
     _call(dev, "etp_group_norm_backward", load_library().etp_group_norm_backward, lmax, c, groups, n, s, _addr(node_ptr),
           dtype, None if kept else x.data_ptr(), CKPT_FORMATS[x.format] if kept else 0, _addr(q), _addr(scale),
           stats.data_ptr(), _addr(weight), _addr(bias), act, grad_out.data_ptr(), int(made),

@@ -1,6 +1,7 @@
 // C ABI of libetp: handle lifecycle, argument checks, workspace carving and kernel dispatch.
 // The operation and conventions are documented in include/etp.h.
 #include <cctype>
+#include <climits>
 #include <cstdlib>
 #include <cstring>
 #include <new>
@@ -869,12 +870,13 @@ etp_status etp_checkpoint_restore(etp_ckpt_format format, etp_dtype dtype, long 
                        static_cast<cudaStream_t>(stream));
 }
 
-size_t etp_group_norm_workspace_bytes(int lmax, int channels, int groups, int backward) {
-  if (!norm::supported(lmax, channels, groups)) return 0;
+size_t etp_group_norm_workspace_bytes(int lmax, int channels, int groups, int n_structs, int backward) {
+  if (!norm::supported(lmax, channels, groups) || n_structs < 0) return 0;
   norm::Call c{};
   c.lmax = lmax;
   c.channels = channels;
   c.groups = groups;
+  c.n_structs = n_structs;
   return norm::workspace_bytes(c, backward != 0);
 }
 
@@ -882,8 +884,8 @@ size_t etp_group_norm_workspace_bytes(int lmax, int channels, int groups, int ba
 static etp_status check_norm(const char* who, const norm::Call& c, etp_ckpt_format format, bool backward,
                              const void* workspace, size_t workspace_bytes) {
   if (!norm::supported(c.lmax, c.channels, c.groups)) {
-    set_error(std::string(who) + ": lmax 0..3; groups <= 64 must divide channels; channels <= 256, or <= 1024 when "
-              "channels and channels / groups are multiples of 4");
+    set_error(std::string(who) + ": lmax 0..3; groups <= 64 must divide channels; rows of at most 4096 values; "
+              "channels <= 256, or <= 1024 when channels and channels / groups are multiples of 4");
     return ETP_ERR_UNSUPPORTED;
   }
   if (!known(c.dtype) || (c.activation != ETP_ACT_NONE && c.activation != ETP_ACT_SILU) ||
@@ -894,6 +896,10 @@ static etp_status check_norm(const char* who, const norm::Call& c, etp_ckpt_form
   if (c.n_nodes < 0 || c.n_structs < 0) {
     set_error(std::string(who) + ": negative size");
     return ETP_ERR_INVALID_ARG;
+  }
+  if (c.n_nodes > INT_MAX - (1 << 16)) {
+    set_error(std::string(who) + ": n_nodes must stay below 2^31 - 2^16");
+    return ETP_ERR_UNSUPPORTED;
   }
   if (!c.node_ptr && c.n_structs != 1) {
     set_error(std::string(who) + ": node_ptr may be NULL only with n_structs = 1");
@@ -920,8 +926,8 @@ etp_status etp_group_norm(int lmax, int channels, int groups, int n_nodes, int n
     set_error(std::string(who) + ": NULL array or negative eps");
     return ETP_ERR_INVALID_ARG;
   }
-  if (!aligned16(x) || !aligned16(out) || reinterpret_cast<uintptr_t>(q) % 4 != 0) {
-    set_error(std::string(who) + ": x and out must be 16-byte aligned, q 4-byte aligned");
+  if (!aligned16(x) || !aligned16(out) || !aligned16(q)) {
+    set_error(std::string(who) + ": x, out and q must be 16-byte aligned");
     return ETP_ERR_INVALID_ARG;
   }
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -929,8 +935,9 @@ etp_status etp_group_norm(int lmax, int channels, int groups, int n_nodes, int n
     return n_structs == 0 ? ETP_OK
                           : cuda_status(cudaMemsetAsync(stats, 0, sizeof(float) * n_structs * (lmax + 2) * groups, s), who);
   if (validate_requested() && (st = norm::validate(c, workspace, s)) != ETP_OK) return st;
-  return norm::forward(c, x, weight, bias, eps, out, stats, format, static_cast<uint8_t*>(q),
-                       static_cast<uint8_t*>(scale), workspace, s);
+  st = norm::forward(c, x, weight, bias, eps, out, stats, format, static_cast<uint8_t*>(q),
+                     static_cast<uint8_t*>(scale), workspace, s);
+  return st == ETP_OK && validate_requested() ? norm::finished(workspace, s, who) : st;
 }
 
 etp_status etp_group_norm_backward(int lmax, int channels, int groups, int n_nodes, int n_structs,
@@ -949,8 +956,8 @@ etp_status etp_group_norm_backward(int lmax, int channels, int groups, int n_nod
     return ETP_ERR_INVALID_ARG;
   }
   if ((format == ETP_CKPT_NONE && !aligned16(x)) || !aligned16(grad_out) || !aligned16(grad_x) ||
-      (format != ETP_CKPT_NONE && reinterpret_cast<uintptr_t>(q) % 4 != 0)) {
-    set_error(std::string(who) + ": x, grad_out and grad_x must be 16-byte aligned, q 4-byte aligned");
+      (format != ETP_CKPT_NONE && (!aligned16(q) || !aligned16(scale)))) {
+    set_error(std::string(who) + ": x, grad_out, grad_x, q and scale must be 16-byte aligned");
     return ETP_ERR_INVALID_ARG;
   }
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -960,8 +967,9 @@ etp_status etp_group_norm_backward(int lmax, int channels, int groups, int n_nod
     return cuda_status(e, who);
   }
   if (validate_requested() && (st = norm::validate(c, workspace, s)) != ETP_OK) return st;
-  return norm::backward(c, x, format, static_cast<const uint8_t*>(q), static_cast<const uint8_t*>(scale), stats, weight,
-                        bias, grad_out, grad_x, grad_weight, grad_bias, workspace, s);
+  st = norm::backward(c, x, format, static_cast<const uint8_t*>(q), static_cast<const uint8_t*>(scale), stats, weight,
+                      bias, grad_out, grad_x, grad_weight, grad_bias, workspace, s);
+  return st == ETP_OK && validate_requested() ? norm::finished(workspace, s, who) : st;
 }
 
 etp_status etp_radial_weights(etp_handle h, int n_edges, const float* edge_vec, const float* W,

@@ -7,7 +7,8 @@ namespace etp {
 namespace norm {
 
 constexpr int kMaxGroups = 64;
-constexpr int kMaxBlocks = 148 * 8;   // more than run at once; the workspace holds this many partials
+constexpr int kMaxVectors = 256;  // 4 (or single) channels a thread: C at most 1024 (256)
+constexpr int kMaxBlocks = 512;   // more than run at once; the workspace holds this many partials
 
 struct Call {
   int lmax, channels, groups, n_nodes, n_structs;
@@ -16,6 +17,8 @@ struct Call {
   int activation, zero_rest;
 };
 
+// ETP_ERR_CUDA if a bounded wait of the call that used ws gave up (synchronises s).
+etp_status finished(void* ws, cudaStream_t s, const char* who);
 bool supported(int lmax, int channels, int groups);
 // ETP_ERR_BAD_GRAPH unless node_ptr ascends within [0, n_nodes] (synchronises s).
 etp_status validate(const Call& c, void* ws, cudaStream_t s);

@@ -303,9 +303,9 @@ etp_status etp_checkpoint_store(etp_ckpt_format format, etp_dtype dtype, long lo
 etp_status etp_checkpoint_restore(etp_ckpt_format format, etp_dtype dtype, long long rows, int cols, const void* q,
                                   const void* scale, void* x, void* stream);
 
-/* Workspace of etp_group_norm (backward = 0) or etp_group_norm_backward (1) for any number of nodes
- * and structures; 0 for shapes that are not supported. */
-size_t etp_group_norm_workspace_bytes(int lmax, int channels, int groups, int backward);
+/* Workspace of etp_group_norm (backward = 0) or etp_group_norm_backward (1) for any number of nodes;
+ * 0 for shapes that are not supported. */
+size_t etp_group_norm_workspace_bytes(int lmax, int channels, int groups, int n_structs, int backward);
 
 /* Group norm with an activation on node rows x[n_nodes][dim], dim = channels (lmax + 1)^2, in the
  * uniform layout. Structure s is the rows node_ptr[s] .. node_ptr[s+1] - 1 (node_ptr: [n_structs + 1]
@@ -321,12 +321,12 @@ size_t etp_group_norm_workspace_bytes(int lmax, int channels, int groups, int ba
  * 16-byte aligned; out may not overlap x. stats[n_structs][lmax + 2][groups] (float32) receives mu,
  * r_0 .. r_lmax; zeros for a structure without rows. Rows that belong to no structure are left as
  * they were in out, or zeroed if zero_rest is nonzero. format: ETP_CKPT_NONE, or the checkpoint of all
- * rows of x is stored to q and scale as by etp_checkpoint_store (q 4-byte aligned), in the same pass
- * when channels % 32 == 0. lmax 0..3; channels / groups whole, groups <= 64, channels <= 256, or
- * <= 1024 when channels and channels / groups are multiples of 4; eps >= 0. Sums are 64-bit; equal
+ * rows of x is stored to q and scale as by etp_checkpoint_store (q 16-byte aligned), in the same
+ * pass when channels % 32 == 0. lmax 0..3; channels / groups whole, groups <= 64, dim <= 4096, channels
+ * <= 256, or <= 1024 when channels and channels / groups are multiples of 4; eps >= 0. Sums are 64-bit; equal
  * calls give equal bits. Asynchronous (a cooperative launch); concurrent calls need their own
- * workspace, 256-byte aligned. With ETP_VALIDATE=1 node_ptr is checked first (ETP_ERR_BAD_GRAPH; the
- * stream is synchronised). */
+ * workspace, 256-byte aligned. With ETP_VALIDATE=1 node_ptr is checked first (ETP_ERR_BAD_GRAPH), and
+ * the call waits and returns ETP_ERR_CUDA if a bounded pipeline wait gave up. */
 etp_status etp_group_norm(int lmax, int channels, int groups, int n_nodes, int n_structs, const int* node_ptr,
                           etp_dtype dtype, const void* x, const float* weight, const float* bias, float eps,
                           etp_activation activation, int zero_rest, void* out, float* stats, etp_ckpt_format format,
@@ -336,7 +336,8 @@ etp_status etp_group_norm(int lmax, int channels, int groups, int n_nodes, int n
  * grad_weight[lmax + 1][channels], grad_bias[channels] (float32, sums over all structures). Any may be
  * NULL, not all three. stats: from the forward. format ETP_CKPT_NONE: x is the forward's input;
  * otherwise x is ignored and the input is read from its checkpoint q, scale. Rows of no structure add
- * nothing; zero_rest as above, for grad_x. grad_x may not overlap grad_out or x. */
+ * nothing; zero_rest as above, for grad_x. grad_x may not overlap grad_out or x.
+ * x, grad_out, grad_x, q, scale: 16-byte aligned. */
 etp_status etp_group_norm_backward(int lmax, int channels, int groups, int n_nodes, int n_structs,
                                    const int* node_ptr, etp_dtype dtype, const void* x, etp_ckpt_format format,
                                    const void* q, const void* scale, const float* stats, const float* weight,

@@ -63,17 +63,17 @@ def test_norm_commutes_with_rotations():
 
 def test_library_refuses_bad_norm_arguments_before_device_work():
     lib, fake, odd = etp.load_library(), ctypes.c_void_p(4096), ctypes.c_void_p(4100)
-    nb = lib.etp_group_norm_workspace_bytes(2, 64, 8, 0)
-    assert nb > 0 and lib.etp_group_norm_workspace_bytes(2, 64, 8, 1) > nb
+    nb = lib.etp_group_norm_workspace_bytes(2, 64, 8, 1, 0)
+    assert nb > 0 and lib.etp_group_norm_workspace_bytes(2, 64, 8, 1, 1) > nb
 
     def fwd(lmax=2, c=64, g=8, n=10, s=1, ptr=None, dtype=0, x=fake, eps=1e-5, act=1, out=fake, stats=fake, fmt=0,
             q=None, scale=None, ws=fake, nb=1 << 30):
         return lib.etp_group_norm(lmax, c, g, n, s, ptr, dtype, x, None, None, eps, act, 0, out, stats, fmt, q, scale,
                                   ws, nb, None)
     for bad in (dict(lmax=4), dict(lmax=-1), dict(g=7), dict(g=0), dict(c=1028, g=1), dict(c=260, g=65),
-                dict(c=258, g=1), dict(c=512, g=256)):
+                dict(c=258, g=1), dict(c=512, g=256), dict(lmax=3, c=260, g=1)):
         assert fwd(**bad) == 3, bad
-        assert lib.etp_group_norm_workspace_bytes(bad.get("lmax", 2), bad.get("c", 64), bad.get("g", 8), 0) == 0, bad
+        assert lib.etp_group_norm_workspace_bytes(bad.get("lmax", 2), bad.get("c", 64), bad.get("g", 8), 1, 0) == 0, bad
     for bad in (dict(n=-1), dict(s=-1, ptr=fake), dict(s=2), dict(dtype=3), dict(act=2), dict(fmt=3), dict(x=None),
                 dict(out=None), dict(stats=None), dict(x=odd), dict(out=odd), dict(eps=-1.0), dict(eps=float("nan")),
                 dict(fmt=1), dict(fmt=1, q=ctypes.c_void_p(4097), scale=fake), dict(ws=None), dict(nb=nb - 1),
@@ -401,7 +401,7 @@ def test_views_other_streams_and_workspace():
     torch.cuda.synchronize()
     for r in got:
         assert all(torch.equal(p, q) for p, q in zip(r, want[:2] + back))
-    ws = torch.empty(etp.group_norm_workspace_bytes(1, 24, 3, backward=True), dtype=torch.uint8, device=DEV).fill_(255)
+    ws = torch.empty(etp.group_norm_workspace_bytes(1, 24, 3, 1, backward=True), dtype=torch.uint8, device=DEV).fill_(255)
     assert torch.equal(etp.group_norm(xd, wd, bd, 1, 3, workspace=ws)[0], want[0])
     assert torch.equal(etp.group_norm_backward(xd, want[1], wd, bd, gd, 1, 3, workspace=ws)[0], back[0])
 
