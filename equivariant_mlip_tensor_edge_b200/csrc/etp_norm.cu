@@ -25,8 +25,8 @@
 //
 // A thread holds V neighbouring channels (V = 4 where channels and group size divide by 4, else 1) of
 // every rp-th row and walks the row's components, so a channel's gate stays in its thread. Sums stay in
-// the thread's registers until its last row of a structure, which leaves them in shared memory; the warp
-// that comes last through a tile where a structure ends adds them up while the others go on.
+// the thread's registers until its last row of a structure, which leaves them in shared memory. The
+// warps meet to add them up once for the rows that the ring holds, not at every structure's end.
 #include <cooperative_groups.h>
 
 #include <climits>
@@ -49,7 +49,7 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kMaxSlots = 16;
 constexpr int kMaxTileRows = 64;
 constexpr int kTileBytes = 24 * 1024;     // aim of a tile
-constexpr int kStreams = 3;
+constexpr int kMaxStreams = 3;
 constexpr int kBlocksPerSm = 1;
 constexpr int kSmem = (227 / kBlocksPerSm - 1) * 1024;   // dynamic, for a block
 
@@ -65,10 +65,10 @@ struct Shape {
 // row, in a ring as long as the rows that warps can be apart.
 struct Ring {
   int tile_rows, slots, slot_bytes, acc_rows, acc_bytes;
-  int off[kStreams];
+  int off[kMaxStreams];
   int o_rows, o_ends, o_sum, o_edge, o_acc, o_ring, bytes;
-  const char* src[kStreams];
-  int row_bytes[kStreams];        // 0: stream not used
+  const char* src[kMaxStreams];
+  int row_bytes[kMaxStreams];        // 0: stream not used
 };
 
 // A structure's end inside a block's rows: rows [a, b) of it lie in the block. slot < 0: all of it;
@@ -116,8 +116,9 @@ __device__ void ended_by(const Shape& s, int ra, int rb, int* na, int* nb) {
 
 struct Shared {
   uint64_t full[kMaxSlots], empty[kMaxSlots];
-  int4 tile[kMaxSlots];              // structure of all rows (-1: of none) or kMixed, its end, ends, -
-  int through[kMaxSlots], copies[kMaxSlots];
+  int4 tile[kMaxSlots];              // structure of all rows or kMixed, its end, structures ended so far, -
+  uint64_t gate;
+  int copies[kMaxSlots];
   int abort, first, behind;          // structures that end in the block's rows: [first, behind)
   int head, tail;                    // structures that cross the block's first / last row, or -1
 };
@@ -127,11 +128,36 @@ constexpr int kMixed = -2;
 struct Turn {
   int slot;
   uint32_t parity;
+  __device__ void next(int slots) {
+    if (++slot == slots) {
+      slot = 0;
+      parity ^= 1u;
+    }
+  }
+};
+
+// The compute warps meet here while copies are under way. A barrier with a bounded wait, unlike the
+// hardware's: a warp that gave up on a copy does not come.
+struct Gate {
+  uint32_t parity = 0;
+  __device__ bool meet(Shared* sh, int* err) {
+    __syncwarp();
+    tc::mbar_arrive_lane0(&sh->gate, threadIdx.x & 31);
+    const bool ok = tc::warp_wait(&sh->gate, parity, &sh->abort, err, 3);
+    parity ^= 1u;
+    return ok;
+  }
 };
 
 __device__ __forceinline__ void meet_compute() { asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory"); }
 
 __device__ __forceinline__ float logistic(float t) { return __fdividef(1.0f, 1.0f + __expf(-t)); }
+
+// 1 / v for a count: a 32-bit reciprocal and one Newton step, 2^-46 off
+__device__ __forceinline__ double reciprocal(double v) {
+  const double r = __frcp_rn(static_cast<float>(v));
+  return fma(r, fma(-v, r, 1.0), r);
+}
 
 template <class T, int V>
 __device__ __forceinline__ void lds_v(const char* p, float (&v)[V]) {
@@ -178,8 +204,9 @@ struct Place {
 
 template <class T, int L, int V>
 struct Fwd {
-  static constexpr int K = (L + 1) * (L + 1), Q = L + 2;
+  static constexpr int K = (L + 1) * (L + 1), Q = L + 2, kStreams = 1;
   static constexpr bool kBackward = false;
+  using Sum = double;
   static constexpr int kLanes = kCkptBlock / V;   // threads that share a checkpoint block
 
   static constexpr int kAcc = 16 + 4 * L;         // bytes of a thread's sums: two of 64 bits, L of 32
@@ -240,11 +267,11 @@ struct Fwd {
 
   // Statistics of rank l of n rows of a group, from sum x (l = 0) and sum x^2: r_l, and mu for l = 0.
   static __device__ float2 value(const Args& p, int l, int n, double s0, double s1) {
-    const double inv = 1.0 / (static_cast<double>(n) * p.s.cg * (2 * l + 1));
+    const double inv = reciprocal(static_cast<double>(n) * p.s.cg * (2 * l + 1));
     const double m = l == 0 ? s0 * inv : 0.0;
     double var = fma(-m, m, s1 * inv);
     if (var < 0.0) var = 0.0;   // not fmax, which would drop a NaN
-    return make_float2(static_cast<float>(m), static_cast<float>(rsqrt(var + static_cast<double>(p.eps))));
+    return make_float2(static_cast<float>(m), rsqrtf(static_cast<float>(var + static_cast<double>(p.eps))));
   }
 
   __device__ void enter_down(const Args& p, const Place& at, int, const float* st) {
@@ -301,8 +328,9 @@ struct Fwd {
 // Streams: grad_out, x or its codes, the codes' scales.
 template <class T, int L, int V, bool kKept>
 struct Bwd {
-  static constexpr int K = (L + 1) * (L + 1), Q = L + 2;
+  static constexpr int K = (L + 1) * (L + 1), Q = L + 2, kStreams = kKept ? 3 : 2;
   static constexpr bool kBackward = true;
+  using Sum = float;
 
   static constexpr int kAcc = 4 * Q;
 
@@ -401,13 +429,13 @@ struct Bwd {
       f[q * cv + i] = t;
     }
   }
-  static __device__ __forceinline__ double first(const char* acc, int, int i) { return reinterpret_cast<const float*>(acc)[i]; }
-  static __device__ __forceinline__ double second(const char* acc, int cv, int l, int i) {
+  static __device__ __forceinline__ float first(const char* acc, int, int i) { return reinterpret_cast<const float*>(acc)[i]; }
+  static __device__ __forceinline__ float second(const char* acc, int cv, int l, int i) {
     return reinterpret_cast<const float*>(acc)[(1 + l) * cv + i];
   }
   // mean h (l = 0) and mean h xhat
   static __device__ float2 value(const Args& p, int l, int n, double s0, double s1) {
-    const double inv = 1.0 / (static_cast<double>(n) * p.s.cg * (2 * l + 1));
+    const double inv = reciprocal(static_cast<double>(n) * p.s.cg * (2 * l + 1));
     return make_float2(static_cast<float>(s0 * inv), static_cast<float>(s1 * inv));
   }
   __device__ void enter_down(const Args& p, const Place& at, int structure, const float* means) {
@@ -452,6 +480,7 @@ __device__ __forceinline__ Turn turn_of(const Ring& ring, int tiles, int tile, b
 
 // Starts a tile's copies into its slot, a lane to a stream: the aligned bytes around the tile, and by
 // hand the last bytes of an array that do not fill 16.
+template <int kStreams>
 __device__ __forceinline__ void copy_tile(const Args& p, Shared* sh, char* smem, int slot, int t0, int t1) {
   const Ring& ring = p.ring;
   const int lane = threadIdx.x & 31;
@@ -475,23 +504,25 @@ __device__ __forceinline__ void copy_tile(const Args& p, Shared* sh, char* smem,
   }
 }
 
-// Writes the tables of a tile: the structure of every row, and the structures that end here. `last`
-// keeps the structure found last, which covers whole tiles of a large one.
+// Writes the tables of a tile: the structure of every row, and the structures that end here, after the
+// *ended of the tiles before. `last` keeps the structure found last, which covers whole tiles of a large
+// one.
 __device__ __forceinline__ void describe_tile(const Args& p, const Work& w, Shared* sh, char* smem, int slot, int t0,
-                                              int t1, End* last) {
+                                              int t1, End* last, int* ended) {
   const Shape& s = p.s;
   const Ring& ring = p.ring;
   const int lane = threadIdx.x & 31;
-  End* ends = reinterpret_cast<End*>(smem + ring.o_ends) + slot * ring.tile_rows;
+  End* ends = reinterpret_cast<End*>(smem + ring.o_ends);
+  const int room = ring.slots * ring.tile_rows;
   if (last->structure >= 0 && last->a <= t0 && last->b >= t1) {
+    const int n_ends = last->b == t1;
     if (lane == 0) {
-      const int n_ends = last->b == t1;
-      if (n_ends) ends[0] = *last;
-      sh->tile[slot] = make_int4(last->structure, last->b, n_ends, 0);
+      if (n_ends) ends[*ended % room] = *last;
+      sh->tile[slot] = make_int4(last->structure, last->b, *ended + n_ends, 0);
     }
+    *ended += n_ends;
   } else {
     int2* rows = reinterpret_cast<int2*>(smem + ring.o_rows) + slot * ring.tile_rows;
-    int n_ends = 0;
     for (int base = t0; base < t1; base += 32) {
       const int n = base + lane;
       int lo = sh->first, hi = sh->behind;      // the first structure that ends behind row n
@@ -513,8 +544,8 @@ __device__ __forceinline__ void describe_tile(const Args& p, const Work& w, Shar
       const bool ends_here = end.structure >= 0 && end.b == n + 1;
       const unsigned votes = __ballot_sync(0xffffffffu, ends_here);
       if (n < t1) rows[n - t0] = make_int2(end.structure, end.b);
-      if (ends_here) ends[n_ends + __popc(votes & ((1u << lane) - 1u))] = end;
-      n_ends += __popc(votes);
+      if (ends_here) ends[(*ended + __popc(votes & ((1u << lane) - 1u))) % room] = end;
+      *ended += __popc(votes);
       const int from = min(31, t1 - 1 - base);
       last->structure = __shfl_sync(0xffffffffu, end.structure, from);
       last->a = __shfl_sync(0xffffffffu, end.a, from);
@@ -522,44 +553,56 @@ __device__ __forceinline__ void describe_tile(const Args& p, const Work& w, Shar
       last->slot = __shfl_sync(0xffffffffu, end.slot, from);
     }
     const bool one = last->structure >= 0 && last->a <= t0;   // and it reaches to the last row
-    if (lane == 0) sh->tile[slot] = make_int4(one ? last->structure : kMixed, last->b, n_ends, 0);
+    if (lane == 0) sh->tile[slot] = make_int4(one ? last->structure : kMixed, last->b, *ended, 0);
   }
   __syncwarp();
   tc::mbar_arrive_lane0(&sh->full[slot], lane);
 }
 
-// The sums of the structures that end in a tile, by one warp, from the threads' sums at their last rows
-// (the last rp rows of a structure hold one of every thread): several lanes to a group and rank, then
-// the statistics, or partial sums where the structure crosses blocks.
+// The sums of the structures ended with numbers [from, to), by all warps, from the threads' sums at their
+// last rows (the last rp rows of a structure hold one of every thread): several lanes to a group and
+// rank, then the statistics, or partial sums where the structure crosses blocks.
 template <class Op>
-__device__ void close(const Args& p, const Work& w, const char* acc, const End* ends, int n_ends) {
+__device__ void close(const Args& p, const Work& w, const char* acc, const End* ends, int from, int to) {
   constexpr int kRanks = Op::Q - 1;
+  using Sum = typename Op::Sum;
   const Shape& s = p.s;
   const int G = s.groups, nq = Op::Q * G, cvg = s.cv / G, lane = threadIdx.x & 31;
-  const int per = kRanks * G, items = n_ends * per;
+  const int per = kRanks * G, items = (to - from) * per, room = p.ring.slots * p.ring.tile_rows;
   int parts = 1;
-  while (parts < 32 && items * parts * 2 <= 32) parts *= 2;
-  for (int base = 0; base < items; base += 32 / parts) {
+  while (parts < 32 && items * parts * 2 <= kThreads) parts *= 2;
+  for (int base = (threadIdx.x / 32) * (32 / parts); base < items; base += kThreads / parts) {
     const int it = base + lane / parts, part = lane & (parts - 1);
-    double s0 = 0.0, s1 = 0.0;
+    Sum a0 = 0, a1 = 0, b0 = 0, b1 = 0;     // two chains each: a sum waits for its last addend, not for its loads
     End e{-1, 0, 0, -1};
     int l = 0, g = 0;
     if (it < items) {
       const int k = it / per;
-      e = ends[k];
+      e = ends[(from + k) % room];
       l = (it - k * per) / G;
       g = it - k * per - l * G;
       const int rows = min(s.rp, e.b - e.a);
-      int at = (e.b - rows - w.r0) % p.ring.acc_rows;
-      for (int r = 0; r < rows; ++r) {
+      int at = (e.b - rows - w.r0 + part) % p.ring.acc_rows;
+      for (int r = part; r < rows; r += parts) {
         const char* row = acc + static_cast<size_t>(at) * p.ring.acc_bytes;
-        if (++at == p.ring.acc_rows) at = 0;
-        for (int j = part; j < cvg; j += parts) {
-          if (l == 0) s0 += Op::first(row, s.cv, g * cvg + j);
-          s1 += Op::second(row, s.cv, l, g * cvg + j);
+        at += parts;
+        if (at >= p.ring.acc_rows) at -= p.ring.acc_rows;
+        int j = g * cvg;
+        for (const int end = j + cvg - 1; j < end; j += 2) {
+          if (l == 0) {
+            a0 += Op::first(row, s.cv, j);
+            b0 += Op::first(row, s.cv, j + 1);
+          }
+          a1 += Op::second(row, s.cv, l, j);
+          b1 += Op::second(row, s.cv, l, j + 1);
+        }
+        if (cvg & 1) {
+          if (l == 0) a0 += Op::first(row, s.cv, j);
+          a1 += Op::second(row, s.cv, l, j);
         }
       }
     }
+    double s0 = static_cast<double>(a0) + b0, s1 = static_cast<double>(a1) + b1;
     for (int o = parts / 2; o > 0; o /= 2) {
       s0 += __shfl_xor_sync(0xffffffffu, s0, o);
       s1 += __shfl_xor_sync(0xffffffffu, s1, o);
@@ -567,13 +610,13 @@ __device__ void close(const Args& p, const Work& w, const char* acc, const End* 
     if (part == 0 && it < items) {
       if (e.slot < 0) {
         const float2 v = Op::value(p, l, e.b - e.a, s0, s1);
-        float* to = p.table + static_cast<size_t>(e.structure) * nq + g;
-        if (l == 0) to[0] = v.x;
-        to[(1 + l) * G] = v.y;
+        float* at = p.table + static_cast<size_t>(e.structure) * nq + g;
+        if (l == 0) at[0] = v.x;
+        at[(1 + l) * G] = v.y;
       } else {
-        double* to = p.part + (static_cast<size_t>(blockIdx.x) * 2 + e.slot) * nq + g;
-        if (l == 0) to[0] = s0;
-        to[(1 + l) * G] = s1;
+        double* at = p.part + (static_cast<size_t>(blockIdx.x) * 2 + e.slot) * nq + g;
+        if (l == 0) at[0] = s0;
+        at[(1 + l) * G] = s1;
       }
     }
   }
@@ -616,7 +659,7 @@ __device__ void gather_partials(const Shape& s, const double* part, int nq, int 
 
 template <class Op, int V>
 __global__ void __launch_bounds__(kBlock, kBlocksPerSm) k_norm(const __grid_constant__ Args p) {
-  constexpr int Q = Op::Q;
+  constexpr int Q = Op::Q, kStreams = Op::kStreams;
   extern __shared__ __align__(128) char smem[];
   __shared__ Shared sh;
   const Shape& s = p.s;
@@ -633,8 +676,9 @@ __global__ void __launch_bounds__(kBlock, kBlocksPerSm) k_norm(const __grid_cons
       for (int k = 0; k < ring.slots; ++k) {
         tc::mbar_init(&sh.full[k], kStreams + 1);
         tc::mbar_init(&sh.empty[k], kWarps);
-        sh.copies[k] = sh.through[k] = 0;
+        sh.copies[k] = 0;
       }
+      tc::mbar_init(&sh.gate, kWarps);
       sh.abort = 0;
       if (blockIdx.x == 0) *p.err = 0;
       asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -642,36 +686,35 @@ __global__ void __launch_bounds__(kBlock, kBlocksPerSm) k_norm(const __grid_cons
     __syncwarp();
     for (int k = 0; k < held; ++k) {
       const int t0 = w.r0 + k * ring.tile_rows;
-      copy_tile(p, &sh, smem, k, t0, min(t0 + ring.tile_rows, w.r1));
+      copy_tile<kStreams>(p, &sh, smem, k, t0, min(t0 + ring.tile_rows, w.r1));
     }
     __syncthreads();
     End last{-1, 0, 0, -1};
     bool ok = true;
+    int ended = 0;
     Turn turn{0, 1};
     for (int k = 0; k < w.tiles; ++k) {
       const int t0 = w.r0 + k * ring.tile_rows, t1 = min(t0 + ring.tile_rows, w.r1);
       if (k >= held) {
         ok = tc::warp_wait(&sh.empty[turn.slot], turn.parity, &sh.abort, p.err, 1);
         if (!ok) break;
-        copy_tile(p, &sh, smem, turn.slot, t0, t1);
+        copy_tile<kStreams>(p, &sh, smem, turn.slot, t0, t1);
       }
-      describe_tile(p, w, &sh, smem, turn.slot, t0, t1, &last);
-      if (++turn.slot == ring.slots) {
-        turn.slot = 0;
-        turn.parity ^= 1u;
-      }
+      describe_tile(p, w, &sh, smem, turn.slot, t0, t1, &last, &ended);
+      turn.next(ring.slots);
     }
     __syncthreads();
     if (gridDim.x > 1) cg::this_grid().sync();
     last.structure = -1;
+    ended = 0;
     if (p.out)
       for (int k = w.tiles - held - 1; k >= 0 && ok; --k) {
         const int t0 = w.r0 + k * ring.tile_rows, t1 = t0 + ring.tile_rows;
         turn = turn_of(ring, w.tiles, k, true);
         ok = tc::warp_wait(&sh.empty[turn.slot], turn.parity ^ 1u, &sh.abort, p.err, 1);
         if (!ok) break;
-        copy_tile(p, &sh, smem, turn.slot, t0, t1);
-        describe_tile(p, w, &sh, smem, turn.slot, t0, t1, &last);
+        copy_tile<kStreams>(p, &sh, smem, turn.slot, t0, t1);
+        describe_tile(p, w, &sh, smem, turn.slot, t0, t1, &last, &ended);
       }
     // the warps that compute wait for every copy, unless one of them gave up
     if (!ok || *static_cast<volatile int*>(&sh.abort))
@@ -700,7 +743,10 @@ __global__ void __launch_bounds__(kBlock, kBlocksPerSm) k_norm(const __grid_cons
   at.col = (threadIdx.x - at.row * s.cv) * V;
   if (at.row >= s.rp) at.col = 0;
   at.g = at.col / s.cg;
-  const int elem[kStreams] = {ring.row_bytes[0] / (Op::K * s.channels), ring.row_bytes[1] / (Op::K * s.channels), 0};
+  // bytes of a value in each stream; a row's scales are indexed from its first
+  int elem[kStreams];
+#pragma unroll
+  for (int k = 0; k < kStreams; ++k) elem[k] = k < 2 ? ring.row_bytes[k] / (Op::K * s.channels) : 0;
   char* acc = smem + ring.o_acc;
   double* sum = reinterpret_cast<double*>(smem + ring.o_sum);
   float* edge = reinterpret_cast<float*>(smem + ring.o_edge);
@@ -723,52 +769,75 @@ __global__ void __launch_bounds__(kBlock, kBlocksPerSm) k_norm(const __grid_cons
         for (int k = 0; k < nq; ++k) p.table[i * nq + k] = 0.0f;
   __syncthreads();
 
-  int current = -1;
+  int step[kStreams];
+#pragma unroll
+  for (int k = 0; k < kStreams; ++k) step[k] = s.rp * ring.row_bytes[k];
+  auto leave = [&](int row) {
+    op.leave(acc + static_cast<size_t>((row - w.r0) % ring.acc_rows) * ring.acc_bytes, s.cv, at.col / V);
+    op.clear();
+  };
+  // A slot is free once the structures that end in its tile are summed up: no warp can then be so far
+  // ahead that it overwrites what the threads left. Where the ring is shorter than the block's rows, half
+  // of it waits for that while the other half is read.
+  const int half = ring.slots / 2;
+  int current = -1, released = 0, closed = 0, ended = 0;
   int n = at.row < s.rp ? w.r0 + at.row : INT_MAX;
-  Turn turn{0, 0};
+  Turn turn{0, 0}, release{0, 0};
+  Gate gate;
   for (int tile = 0; tile < w.tiles; ++tile) {
     const int slot = turn.slot, t0 = w.r0 + tile * ring.tile_rows, t1 = min(t0 + ring.tile_rows, w.r1);
     if (!tc::warp_wait(&sh.full[slot], turn.parity, &sh.abort, p.err, 2)) break;
     const int4 about = sh.tile[slot];
     if (n < t1) {
-      const char* base[kStreams];
-      sources(slot, t0, base);
-      for (; n < t1; n += s.rp) {
-        int2 e = make_int2(about.x, about.y);
-        if (about.x == kMixed) e = rows[slot * ring.tile_rows + n - t0];
-        if (e.x < 0) continue;
-        if (e.x != current) {
-          current = e.x;
+      const char* src[kStreams];
+      sources(slot, t0, src);
+#pragma unroll
+      for (int k = 0; k < kStreams; ++k) src[k] += (n - t0) * ring.row_bytes[k];
+      if (about.x != kMixed) {
+        if (about.x != current) {
+          current = about.x;
           op.enter_up(p, at, current);
         }
-        const char* src[kStreams];
+        do {
+          op.add(p, at, src, at.col);
+          n += s.rp;
 #pragma unroll
-        for (int k = 0; k < kStreams; ++k) src[k] = base[k] + (n - t0) * ring.row_bytes[k];
-        op.add(p, at, src, at.col);
-        if (n + s.rp >= e.y) {
-          op.leave(acc + static_cast<size_t>((n - w.r0) % ring.acc_rows) * ring.acc_bytes, s.cv, at.col / V);
-          op.clear();
+          for (int k = 0; k < kStreams; ++k) src[k] += step[k];
+        } while (n < t1);
+        if (n >= about.y) leave(n - s.rp);
+      } else {
+        for (; n < t1; n += s.rp) {
+          const int2 e = rows[slot * ring.tile_rows + n - t0];
+          if (e.x >= 0) {
+            if (e.x != current) {
+              current = e.x;
+              op.enter_up(p, at, current);
+            }
+            op.add(p, at, src, at.col);
+            if (n + s.rp >= e.y) leave(n);
+          }
+#pragma unroll
+          for (int k = 0; k < kStreams; ++k) src[k] += step[k];
         }
       }
     }
-    __syncwarp();
-    if (about.z > 0) {
-      int before = 0;
-      __threadfence_block();
-      if (lane == 0) before = atomicAdd(&sh.through[slot], 1);
-      if (__shfl_sync(0xffffffffu, before, 0) == kWarps - 1) {
-        __threadfence_block();
-        close<Op>(p, w, acc, ends + slot * ring.tile_rows, about.z);
-        if (lane == 0) sh.through[slot] = 0;
-        __syncwarp();
+    ended = about.z;
+    turn.next(ring.slots);
+    if (released < w.tiles - ring.slots && (ended == closed || tile - released + 1 >= half)) {
+      if (ended > closed) {
+        if (!gate.meet(&sh, p.err)) break;
+        close<Op>(p, w, acc, ends, closed, ended);
+        closed = ended;
+      }
+      __syncwarp();
+      for (; released <= tile && released < w.tiles - ring.slots; ++released) {
+        tc::mbar_arrive_lane0(&sh.empty[release.slot], lane);
+        release.next(ring.slots);
       }
     }
-    if (tile < w.tiles - ring.slots) tc::mbar_arrive_lane0(&sh.empty[slot], lane);
-    if (++turn.slot == ring.slots) {
-      turn.slot = 0;
-      turn.parity ^= 1u;
-    }
   }
+  meet_compute();
+  if (!*static_cast<volatile int*>(&sh.abort) && ended > closed) close<Op>(p, w, acc, ends, closed, ended);
   if constexpr (Op::kBackward) {
     // the block's channel sums, over the rows it reads side by side
     float* flat = reinterpret_cast<float*>(sum);
@@ -834,7 +903,7 @@ __global__ void __launch_bounds__(kBlock, kBlocksPerSm) k_norm(const __grid_cons
   current = -1;
   // the last row of this thread
   n = at.row < s.rp && at.row < w.r1 - w.r0 ? w.r0 + at.row + (w.r1 - w.r0 - 1 - at.row) / s.rp * s.rp : -1;
-  turn = turn_of(ring, w.tiles, max(0, w.tiles - 1), false);
+  turn = turn_of(ring, w.tiles, w.tiles - 1, false);
   for (int tile = w.tiles - 1; tile >= 0; --tile) {
     const int slot = turn.slot, t0 = w.r0 + tile * ring.tile_rows;
     if (tile < w.tiles - ring.slots &&
@@ -842,19 +911,32 @@ __global__ void __launch_bounds__(kBlock, kBlocksPerSm) k_norm(const __grid_cons
       return;
     if (n >= t0) {
       const int about = sh.tile[slot].x;
-      const char* base[kStreams];
-      sources(slot, t0, base);
-      for (; n >= t0; n -= s.rp) {
-        const int i = about == kMixed ? rows[slot * ring.tile_rows + n - t0].x : about;
-        if (i < 0 && !op.wants_outside(p)) continue;
-        if (i >= 0 && i != current) {
+      const char* src[kStreams];
+      sources(slot, t0, src);
+#pragma unroll
+      for (int k = 0; k < kStreams; ++k) src[k] += (n - t0) * ring.row_bytes[k];
+      auto enter = [&](int i) {
+        if (i != current) {
           current = i;
           op.enter_down(p, at, i, i == sh.head ? edge : i == sh.tail ? edge + nq : p.table + static_cast<size_t>(i) * nq);
         }
-        const char* src[kStreams];
+      };
+      if (about != kMixed) {
+        enter(about);
+        do {
+          op.put(p, at, src, at.col, n, true);
+          n -= s.rp;
 #pragma unroll
-        for (int k = 0; k < kStreams; ++k) src[k] = base[k] + (n - t0) * ring.row_bytes[k];
-        op.put(p, at, src, at.col, n, i >= 0);
+          for (int k = 0; k < kStreams; ++k) src[k] -= step[k];
+        } while (n >= t0);
+      } else {
+        for (; n >= t0; n -= s.rp) {
+          const int i = rows[slot * ring.tile_rows + n - t0].x;
+          if (i >= 0) enter(i);
+          if (i >= 0 || op.wants_outside(p)) op.put(p, at, src, at.col, n, i >= 0);
+#pragma unroll
+          for (int k = 0; k < kStreams; ++k) src[k] -= step[k];
+        }
       }
     }
     if (tile >= ring.slots) {
@@ -874,14 +956,14 @@ int vector_width(int channels, int groups) {
 int round_up(int v, int to) { return (v + to - 1) / to * to; }
 
 // Shared memory of a call: the sums, and slots with their tables and places for sums in what is left.
-bool plan_ring(const Shape& s, int q, int acc_thread, const int (&row_bytes)[kStreams], Ring* r) {
+bool plan_ring(const Shape& s, int q, int acc_thread, const int (&row_bytes)[kMaxStreams], Ring* r) {
   int per_row = 0;
-  for (int k = 0; k < kStreams; ++k) per_row += row_bytes[k];
+  for (int k = 0; k < kMaxStreams; ++k) per_row += row_bytes[k];
   r->tile_rows = kTileBytes / per_row;
   if (r->tile_rows < 1) r->tile_rows = 1;
   if (r->tile_rows > kMaxTileRows) r->tile_rows = kMaxTileRows;
   int at = 0, in_slot = 0;
-  for (int k = 0; k < kStreams; ++k) {
+  for (int k = 0; k < kMaxStreams; ++k) {
     r->row_bytes[k] = row_bytes[k];
     r->off[k] = in_slot;
     if (row_bytes[k]) in_slot += round_up(row_bytes[k] * r->tile_rows + 32, 128);
@@ -924,7 +1006,7 @@ Shape shape_of(const Call& c, int width) {
 }
 
 template <class Op, int V>
-etp_status launch(const Call& c, Args& p, const int (&row_bytes)[kStreams], cudaStream_t stream, const char* what) {
+etp_status launch(const Call& c, Args& p, const int (&row_bytes)[kMaxStreams], cudaStream_t stream, const char* what) {
   auto kernel = k_norm<Op, V>;
   p.s = shape_of(c, V);
   if (!plan_ring(p.s, Op::Q, Op::kAcc, row_bytes, &p.ring)) {
@@ -962,13 +1044,13 @@ etp_status launch(const Call& c, Args& p, const int (&row_bytes)[kStreams], cuda
 
 template <class T, int L, int V>
 etp_status fwd_launch(const Call& c, Args& p, cudaStream_t s) {
-  const int row_bytes[kStreams] = {Fwd<T, L, V>::K * c.channels * static_cast<int>(sizeof(T)), 0, 0};
+  const int row_bytes[kMaxStreams] = {Fwd<T, L, V>::K * c.channels * static_cast<int>(sizeof(T)), 0, 0};
   return launch<Fwd<T, L, V>, V>(c, p, row_bytes, s, "group norm launch");
 }
 template <class T, int L, int V, bool kKept>
 etp_status bwd_launch(const Call& c, Args& p, cudaStream_t s) {
   const int dim = Bwd<T, L, V, kKept>::K * c.channels, size = static_cast<int>(sizeof(T));
-  const int row_bytes[kStreams] = {dim * size, kKept ? dim : dim * size, kKept ? (dim + kCkptBlock - 1) / kCkptBlock : 0};
+  const int row_bytes[kMaxStreams] = {dim * size, kKept ? dim : dim * size, kKept ? (dim + kCkptBlock - 1) / kCkptBlock : 0};
   return launch<Bwd<T, L, V, kKept>, V>(c, p, row_bytes, s, "group norm backward launch");
 }
 
