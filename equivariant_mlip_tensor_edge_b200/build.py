@@ -16,10 +16,11 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libetp.so")
 SOURCES = ["etp_abi.cu", "etp_graph.cu", "etp_conv.cu", "etp_fwd_tc.cu", "etp_bwd_tc.cu", "etp_noalloc.cu", "etp_dw.cu", "etp_fwd_cx.cu", "etp_ladder_full.cu", "etp_product.cu", "etp_general.cu", "etp_general_tc.cu",
-           "etp_checkpoint.cu", "etp_norm.cu"]
+           "etp_checkpoint.cu", "etp_norm.cu", "etp_norm_fwd.cu", "etp_norm_bwd.cu"]
 HEADERS = [os.path.join(ROOT, "include", "etp.h"), os.path.join(CSRC, "etp_internal.h"),
            os.path.join(CSRC, "generated", "etp_paths.h"), os.path.join(CSRC, "etp_device.h"), os.path.join(CSRC, "etp_tc_common.h"),
-           os.path.join(CSRC, "etp_checkpoint.h"), os.path.join(CSRC, "etp_norm.h")]
+           os.path.join(CSRC, "etp_checkpoint.h"), os.path.join(CSRC, "etp_norm.h"),
+           os.path.join(CSRC, "etp_norm_sweep.h")]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 FLAGS = ["-O3", "-std=c++17", "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo",
          "-Xcompiler", "-fPIC", "-I" + os.path.join(ROOT, "include"), "-I" + CSRC]

@@ -19,9 +19,9 @@ __global__ void __launch_bounds__(kThreads) k_store_whole(long long n_vec, bool 
   for (long long i = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x; i < n_round; i += stride) {
     float v[4] = {0.f, 0.f, 0.f, 0.f};
     if (i < n_vec) load_v<T, 4>(x + i * 4, v);
-    unsigned m = max(max(abs_bits(v[0]), abs_bits(v[1])), max(abs_bits(v[2]), abs_bits(v[3])));
+    float m = max_abs(max_abs(v[0], v[1]), max_abs(v[2], v[3]));
 #pragma unroll
-    for (int o = 1; o < 8; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    for (int o = 1; o < 8; o <<= 1) m = max_abs(m, __shfl_xor_sync(0xffffffffu, m, o));
     const unsigned byte = scale_byte(m, int8);
     if (i < n_vec) {
       reinterpret_cast<unsigned*>(q)[i] = encode4(v, inv_scale(byte), byte == kCkptBad, int8);
@@ -41,7 +41,9 @@ __global__ void __launch_bounds__(kThreads) k_store_any(long long rows, int cols
     const long long row = b / blocks;
     const int col = static_cast<int>(b - row * blocks) * kCkptBlock + lane;
     const float v = col < cols ? to_f32<T>(x[row * cols + col]) : 0.0f;
-    unsigned m = __reduce_max_sync(0xffffffffu, abs_bits(v));
+    float m = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) m = max_abs(m, __shfl_xor_sync(0xffffffffu, m, o));
     const unsigned byte = scale_byte(m, int8);
     if (col < cols) q[row * cols + col] = static_cast<uint8_t>(encode(v, inv_scale(byte), byte == kCkptBad, int8));
     if (lane == 0) scale[b] = static_cast<uint8_t>(byte);
