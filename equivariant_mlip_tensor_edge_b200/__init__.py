@@ -8,6 +8,7 @@ is no CPU fallback: without the built library, or without a CUDA device, calls r
 The C ABI is documented in ``include/etp.h``.
 """
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 
@@ -433,14 +434,14 @@ def _rows(t):
     return t if t.data_ptr() % 16 == 0 else t.clone()
 
 
-def _call(device, where, fn, *args):
-    """Calls a library function with the current stream of ``device``, which is made current for it."""
+def _call(index, where, fn, *args):
+    """Calls a library function on the current stream of device ``index``, which is made current for it."""
     torch = _torch()
-    if torch.cuda.current_device() == device.index:
-        st = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    if torch.cuda.current_device() == index:
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
-        with torch.cuda.device(device):
-            st = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+        with torch.cuda.device(index):
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     if st != ETP_OK:
         raise EtpError(st, where)
 
@@ -449,11 +450,15 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-def _same_device(x, *others):
-    _need_cuda(x, *others)
+def _one_device(x, *others):
+    """Index of the CUDA device that all of the tensors are on."""
+    index = x.get_device()
+    if index < 0:
+        raise ValueError("libetp operates on CUDA tensors only (no CPU fallback)")
     for t in others:
-        if t is not None and t.device != x.device:
+        if t is not None and t.get_device() != index:
             raise ValueError(f"tensors on {x.device} and {t.device} in one call")
+    return index
 
 
 @dataclass
@@ -482,7 +487,7 @@ class Checkpoint8:
 
     def _checked(self):
         torch = _torch()
-        _same_device(self.q, self.scale)
+        _one_device(self.q, self.scale)
         cols = self.q.shape[-1]
         if self.q.dtype not in (torch.int8, torch.float8_e4m3fn) or self.scale.dtype != torch.uint8:
             raise ValueError("a checkpoint has int8 or float8_e4m3fn codes and uint8 scales")
@@ -492,24 +497,22 @@ class Checkpoint8:
 
     def restore(self, dtype=None, out=None):
         """The values the checkpoint stands for, in ``dtype`` (default: that of the activations)."""
-        torch = _torch()
         q, scale = self._checked()
         if out is None:
-            out = torch.empty(q.shape, dtype=dtype or self.dtype, device=q.device)
+            out = q.new_empty(q.shape, dtype=dtype or self.dtype)
         elif out.shape != q.shape or not out.is_contiguous() or (dtype is not None and out.dtype != dtype):
             raise ValueError("out must be contiguous, of the checkpoint's shape and the dtype asked for")
-        _same_device(q, out)
         cols = q.shape[-1]
-        _call(q.device, "etp_checkpoint_restore", load_library().etp_checkpoint_restore, CKPT_FORMATS[self.format],
+        _call(_one_device(q, out), "etp_checkpoint_restore", load_library().etp_checkpoint_restore, CKPT_FORMATS[self.format],
               _dtype_code(out.dtype), q.numel() // max(cols, 1), cols, q.data_ptr(), scale.data_ptr(), out.data_ptr())
         return out
 
 
 def _empty_checkpoint(x, fmt):
     torch = _torch()
-    return Checkpoint8(torch.empty(x.shape, dtype=torch.int8 if fmt == 1 else torch.float8_e4m3fn, device=x.device),
-                       torch.empty(x.shape[:-1] + (-(-x.shape[-1] // CKPT_BLOCK),), dtype=torch.uint8, device=x.device),
-                       x.dtype)
+    shape = x.shape
+    return Checkpoint8(x.new_empty(shape, dtype=torch.int8 if fmt == 1 else torch.float8_e4m3fn),
+                       x.new_empty(shape[:-1] + (-(-shape[-1] // CKPT_BLOCK),), dtype=torch.uint8), x.dtype)
 
 
 def checkpoint8(x, fmt="int8"):
@@ -522,18 +525,19 @@ def checkpoint8(x, fmt="int8"):
     code = _named(CKPT_FORMATS, fmt, "fmt")
     if code == 0:
         raise ValueError("fmt must be 'int8' or 'e4m3'")
-    _need_cuda(x)
+    index = _one_device(x)
     if x.dim() < 1:
         raise ValueError("x needs at least one dimension")
     dtype = _dtype_code(x.dtype)
     x = x.contiguous()
     ck = _empty_checkpoint(x, code)
     cols = x.shape[-1]
-    _call(x.device, "etp_checkpoint_store", load_library().etp_checkpoint_store, code, dtype, x.numel() // max(cols, 1),
+    _call(index, "etp_checkpoint_store", load_library().etp_checkpoint_store, code, dtype, x.numel() // max(cols, 1),
           cols, x.data_ptr(), ck.q.data_ptr(), ck.scale.data_ptr())
     return ck
 
 
+@functools.lru_cache(maxsize=256)
 def group_norm_workspace_bytes(lmax, channels, groups, n_structs=1, backward=False):
     return load_library().etp_group_norm_workspace_bytes(int(lmax), int(channels), int(groups), int(n_structs), int(backward))
 
@@ -556,19 +560,19 @@ def _norm_shape(shape, lmax, groups, node_ptr, weight, bias):
     return n, c, 1 if node_ptr is None else node_ptr.numel() - 1
 
 
-def _norm_workspace(lmax, c, groups, s, backward, device, workspace):
+def _norm_workspace(lmax, c, groups, s, backward, x, workspace):
     nb = group_norm_workspace_bytes(lmax, c, groups, s, backward)
     if workspace is None or workspace.numel() < nb:
-        workspace = _torch().empty(max(nb, 1), dtype=_torch().uint8, device=device)
+        workspace = x.new_empty(max(nb, 1), dtype=_torch().uint8)
     return workspace, nb
 
 
-def _into(out, shape, dtype, device, what):
+def _into(out, shape, dtype, x, what):
     """(tensor to write, whether the library made it)"""
     if out is None:
-        return _torch().empty(shape, dtype=dtype, device=device), True
-    if tuple(out.shape) != tuple(shape) or out.dtype != dtype or out.device != device or not out.is_contiguous():
-        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+        return x.new_empty(shape, dtype=dtype), True
+    if tuple(out.shape) != tuple(shape) or out.dtype != dtype or out.device != x.device or not out.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {x.device}")
     return out, False
 
 
@@ -584,22 +588,20 @@ def group_norm(x, weight, bias, lmax, groups, node_ptr=None, eps=1e-5, activatio
     backward. checkpoint "int8" or "e4m3": also returns the Checkpoint8 of x (else None), in the same
     pass when C % 32 == 0. Rows of no structure: untouched in a given ``out``, zero in a new one.
     """
-    torch = _torch()
-    _same_device(x, weight, bias, node_ptr)
+    index = _one_device(x, weight, bias, node_ptr)
     dtype = _dtype_code(x.dtype)
     n, c, s = _norm_shape(x.shape, lmax, groups, node_ptr, weight, bias)
     act, fmt = _named(ACTIVATIONS, activation, "activation"), _named(CKPT_FORMATS, checkpoint, "checkpoint")
     x = _rows(x)
-    dev = x.device
     weight = None if weight is None else _f32(weight)
     bias = None if bias is None else _f32(bias)
     node_ptr = None if node_ptr is None else _i32(node_ptr)
-    out, made = _into(out, x.shape, x.dtype, dev, "out")
-    stats, _ = _into(stats, (s, lmax + 2, groups), torch.float32, dev, "stats")
+    out, made = _into(out, x.shape, x.dtype, x, "out")
+    stats, _ = _into(stats, (s, lmax + 2, groups), _torch().float32, x, "stats")
     ck = _empty_checkpoint(x, fmt) if fmt else None
-    ws, nb = _norm_workspace(lmax, c, groups, s, False, dev, workspace)
-    _call(dev, "etp_group_norm", load_library().etp_group_norm, lmax, c, groups, n, s, _addr(node_ptr), dtype,
-          x.data_ptr(), _addr(weight), _addr(bias), eps, act, int(made), out.data_ptr(), stats.data_ptr(), fmt,
+    ws, nb = _norm_workspace(lmax, c, groups, s, False, x, workspace)
+    _call(index, "etp_group_norm", load_library().etp_group_norm, lmax, c, groups, n, s, _addr(node_ptr), dtype,
+          x.data_ptr(), _addr(weight), _addr(bias), eps, act, made, out.data_ptr(), stats.data_ptr(), fmt,
           ck.q.data_ptr() if ck else None, ck.scale.data_ptr() if ck else None, ws.data_ptr(), nb)
     return out, stats, ck
 
@@ -612,9 +614,8 @@ def group_norm_backward(x, stats, weight, bias, grad_out, lmax, groups, node_ptr
     grad_weight [lmax+1, C] and grad_bias [C] are float32 sums over all structures (None when
     want_grad_affine is false). Rows of no structure: untouched in a given ``grad_x``, zero in a new one.
     """
-    torch = _torch()
     kept = isinstance(x, Checkpoint8)
-    _same_device(grad_out, x.q if kept else x, stats, weight, bias, node_ptr)
+    index = _one_device(grad_out, x.q if kept else x, stats, weight, bias, node_ptr)
     dtype = _dtype_code(grad_out.dtype)
     n, c, s = _norm_shape(x.shape, lmax, groups, node_ptr, weight, bias)
     act = _named(ACTIVATIONS, activation, "activation")
@@ -624,7 +625,6 @@ def group_norm_backward(x, stats, weight, bias, grad_out, lmax, groups, node_ptr
         raise ValueError(f"stats must be [{s}, {lmax + 2}, {groups}], got {tuple(stats.shape)}")
     if not (want_grad_x or want_grad_affine):
         return None, None, None
-    dev = grad_out.device
     grad_out, stats = _rows(grad_out), _f32(stats)
     q = scale = None
     if kept:
@@ -636,13 +636,13 @@ def group_norm_backward(x, stats, weight, bias, grad_out, lmax, groups, node_ptr
     node_ptr = None if node_ptr is None else _i32(node_ptr)
     made = False
     if want_grad_x:
-        grad_x, made = _into(grad_x, grad_out.shape, grad_out.dtype, dev, "grad_x")
-    gw = torch.empty((lmax + 1, c), dtype=torch.float32, device=dev) if want_grad_affine else None
-    gb = torch.empty(c, dtype=torch.float32, device=dev) if want_grad_affine else None
-    ws, nb = _norm_workspace(lmax, c, groups, s, True, dev, workspace)
-    _call(dev, "etp_group_norm_backward", load_library().etp_group_norm_backward, lmax, c, groups, n, s, _addr(node_ptr),
-          dtype, None if kept else x.data_ptr(), CKPT_FORMATS[x.format] if kept else 0, _addr(q), _addr(scale),
-          stats.data_ptr(), _addr(weight), _addr(bias), act, grad_out.data_ptr(), int(made),
+        grad_x, made = _into(grad_x, grad_out.shape, grad_out.dtype, grad_out, "grad_x")
+    gw = grad_out.new_empty((lmax + 1, c), dtype=_torch().float32) if want_grad_affine else None
+    gb = grad_out.new_empty(c, dtype=_torch().float32) if want_grad_affine else None
+    ws, nb = _norm_workspace(lmax, c, groups, s, True, grad_out, workspace)
+    _call(index, "etp_group_norm_backward", load_library().etp_group_norm_backward, lmax, c, groups, n, s,
+          _addr(node_ptr), dtype, None if kept else x.data_ptr(), CKPT_FORMATS[x.format] if kept else 0, _addr(q),
+          _addr(scale), stats.data_ptr(), _addr(weight), _addr(bias), act, grad_out.data_ptr(), made,
           grad_x.data_ptr() if want_grad_x else None, _addr(gw), _addr(gb), ws.data_ptr(), nb)
     return (grad_x if want_grad_x else None), gw, gb
 

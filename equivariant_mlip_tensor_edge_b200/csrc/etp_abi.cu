@@ -885,7 +885,7 @@ static etp_status check_norm(const char* who, const norm::Call& c, etp_ckpt_form
                              const void* workspace, size_t workspace_bytes) {
   if (!norm::supported(c.lmax, c.channels, c.groups)) {
     set_error(std::string(who) + ": lmax 0..3; groups <= 64 must divide channels; rows of at most 4096 values; "
-              "channels <= 256, or <= 1024 when channels and channels / groups are multiples of 4");
+              "channels <= 1024, 512 or 256 as channels / groups is a multiple of 4, of 2 or odd");
     return ETP_ERR_UNSUPPORTED;
   }
   if (!known(c.dtype) || (c.activation != ETP_ACT_NONE && c.activation != ETP_ACT_SILU) ||

@@ -7,7 +7,7 @@ namespace etp {
 namespace norm {
 
 constexpr int kMaxGroups = 64;
-constexpr int kMaxVectors = 256;  // 4 (or single) channels a thread: C at most 1024 (256)
+constexpr int kMaxVectors = 256;  // of 4, 2 or 1 channels: C at most 1024, 512 or 256
 constexpr int kMaxBlocks = 512;   // more than run at once; the workspace holds this many partials
 
 struct Call {

@@ -323,7 +323,7 @@ size_t etp_group_norm_workspace_bytes(int lmax, int channels, int groups, int n_
  * they were in out, or zeroed if zero_rest is nonzero. format: ETP_CKPT_NONE, or the checkpoint of all
  * rows of x is stored to q and scale as by etp_checkpoint_store (q 16-byte aligned), in the same
  * pass when channels % 32 == 0. lmax 0..3; channels / groups whole, groups <= 64, dim <= 4096, channels
- * <= 256, or <= 1024 when channels and channels / groups are multiples of 4; eps >= 0. Sums are 64-bit; equal
+ * <= 1024, 512 or 256 as channels / groups is a multiple of 4, of 2 or odd; eps >= 0. Sums are 64-bit; equal
  * calls give equal bits. Asynchronous (a cooperative launch); concurrent calls need their own
  * workspace, 256-byte aligned. With ETP_VALIDATE=1 node_ptr is checked first (ETP_ERR_BAD_GRAPH), and
  * the call waits and returns ETP_ERR_CUDA if a bounded pipeline wait gave up. */

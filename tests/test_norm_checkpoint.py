@@ -71,7 +71,7 @@ def test_library_refuses_bad_norm_arguments_before_device_work():
         return lib.etp_group_norm(lmax, c, g, n, s, ptr, dtype, x, None, None, eps, act, 0, out, stats, fmt, q, scale,
                                   ws, nb, None)
     for bad in (dict(lmax=4), dict(lmax=-1), dict(g=7), dict(g=0), dict(c=1028, g=1), dict(c=260, g=65),
-                dict(c=258, g=1), dict(c=512, g=256), dict(lmax=3, c=260, g=1)):
+                dict(c=257, g=1), dict(c=514, g=1), dict(c=512, g=256), dict(lmax=3, c=260, g=1)):
         assert fwd(**bad) == 3, bad
         assert lib.etp_group_norm_workspace_bytes(bad.get("lmax", 2), bad.get("c", 64), bad.get("g", 8), 1, 0) == 0, bad
     for bad in (dict(n=-1), dict(s=-1, ptr=fake), dict(s=2), dict(dtype=3), dict(act=2), dict(fmt=3), dict(x=None),
