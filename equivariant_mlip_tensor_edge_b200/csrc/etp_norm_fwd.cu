@@ -89,7 +89,7 @@ struct Fwd {
     return make_float2(static_cast<float>(m), rsqrtf(static_cast<float>(var + static_cast<double>(p.eps))));
   }
 
-  __device__ void enter_down(const Args& p, const Place& at, int, const float* st) {
+  __device__ __forceinline__ void enter_down(const Args& p, const Place& at, int, const float* st) {
     mu = st[at.g];
 #pragma unroll
     for (int l = 0; l <= L; ++l) {
@@ -99,56 +99,75 @@ struct Fwd {
     }
   }
 
-  static __device__ __forceinline__ void keep(const Args& p, size_t at, const float (&v)[V]) {
-    float top = max_abs(v[0], v[V - 1]);
+  // Checkpoint codes of N vectors of a row, `apart` values from one to the next: N reductions side by side,
+  // as each is a chain of shuffles.
+  template <int N>
+  static __device__ __forceinline__ void keep(const Args& p, size_t at, int apart, const float (&v)[N][V]) {
+    float top[N];
 #pragma unroll
-    for (int k = 1; k < V - 1; ++k) top = max_abs(top, v[k]);
+    for (int i = 0; i < N; ++i) {
+      top[i] = max_abs(v[i][0], v[i][V - 1]);
+#pragma unroll
+      for (int k = 1; k < V - 1; ++k) top[i] = max_abs(top[i], v[i][k]);
+    }
     // the lanes of a block hold the same row, so they are here together
     const unsigned lane = threadIdx.x & 31;
     const unsigned mask = kLanes == 32 ? 0xffffffffu : ((1u << (kLanes & 31)) - 1u) << (lane & (32u - kLanes));
 #pragma unroll
-    for (int o = 1; o < kLanes; o <<= 1) top = max_abs(top, __shfl_xor_sync(mask, top, o));
-    const unsigned byte = scale_byte(top, p.int8);
-    store_codes<V>(p.q + at, v, inv_scale(byte), byte == kCkptBad, p.int8);
-    if ((lane & (kLanes - 1)) == 0) p.scale[at / kCkptBlock] = static_cast<uint8_t>(byte);
+    for (int o = 1; o < kLanes; o <<= 1)
+#pragma unroll
+      for (int i = 0; i < N; ++i) top[i] = max_abs(top[i], __shfl_xor_sync(mask, top[i], o));
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const unsigned byte = scale_byte(top[i], p.int8);
+      const size_t to = at + i * apart;
+      store_codes<V>(p.q + to, v[i], inv_scale(byte), byte == kCkptBad, p.int8);
+      if ((lane & (kLanes - 1)) == 0) p.scale[to / kCkptBlock] = static_cast<uint8_t>(byte);
+    }
+  }
+
+  // components [M, M + N) of a row; f: the gate, made by component 0
+  template <int M, int N>
+  __device__ __forceinline__ void put_part(const Args& p, const char* src, size_t first, bool inside, float (&f)[V]) {
+    const int C = p.s.channels;
+    float v[N][V];
+#pragma unroll
+    for (int i = 0; i < N; ++i) lds_v<T, V>(src + (M + i) * C * static_cast<int>(sizeof(T)), v[i]);
+    if (p.q) keep<N>(p, first + M * C, C, v);
+    if (!inside && !p.zero_rest) return;
+    T* out = static_cast<T*>(p.out) + first + M * C;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int m = M + i, l = m == 0 ? 0 : m < 4 ? 1 : m < 9 ? 2 : 3;
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        if (m == 0) {
+          v[i][k] = fmaf(v[i][k] - mu, wr[0][k], bias[k]);
+          f[k] = p.act ? logistic(v[i][k]) : 1.0f;
+          v[i][k] *= f[k];
+        } else {
+          v[i][k] = v[i][k] * (wr[l <= L ? l : L][k] * f[k]);
+        }
+        if (!inside) v[i][k] = 0.0f;
+      }
+      store_v<T, V>(out + i * C, v[i]);
+    }
   }
 
   // outputs of rows n, n - rp, ..; inside: they belong to a structure
   template <int R>
-  __device__ void put(const Args& p, const Place& at, const char* const (&src)[kStreams], const int (&step)[kStreams], int,
-                      int n, bool inside) {
-    float v[R][V], f[R][V];
-#pragma unroll
-    for (int h = 0; h < R; ++h) lds_v<T, V>(src[0] - h * step[0], v[h]);
+  __device__ __forceinline__ void put(const Args& p, const Place& at, const char* const (&src)[kStreams],
+                                      const int (&step)[kStreams], int, int n, bool inside) {
 #pragma unroll
     for (int h = 0; h < R; ++h) {
       const size_t first = static_cast<size_t>(n - h * p.s.rp) * K * p.s.channels + at.col;
-      if (p.q) keep(p, first, v[h]);
-#pragma unroll
-      for (int k = 0; k < V; ++k) {
-        v[h][k] = fmaf(v[h][k] - mu, wr[0][k], bias[k]);
-        f[h][k] = p.act ? logistic(v[h][k]) : 1.0f;
-        v[h][k] = inside ? v[h][k] * f[h][k] : 0.0f;
-      }
-      if (inside || p.zero_rest) store_v<T, V>(static_cast<T*>(p.out) + first, v[h]);
+      const char* from = src[0] - h * step[0];
+      float f[V];
+      put_part<0, K < 4 ? 1 : 4>(p, from, first, inside, f);
+      if constexpr (K > 4) put_part<4, K == 9 ? 5 : 4>(p, from, first, inside, f);
+      if constexpr (K > 9) put_part<8, 4>(p, from, first, inside, f);
+      if constexpr (K > 9) put_part<12, 4>(p, from, first, inside, f);
     }
-#pragma unroll
-    for (int l = 1; l <= L; ++l)
-#pragma unroll
-      for (int h = 0; h < R; ++h) {
-        const size_t first = static_cast<size_t>(n - h * p.s.rp) * K * p.s.channels + at.col;
-        float c[V];
-#pragma unroll
-        for (int k = 0; k < V; ++k) c[k] = wr[l][k] * f[h][k];
-#pragma unroll
-        for (int m = l * l; m < (l + 1) * (l + 1); ++m) {
-          lds_v<T, V>(src[0] - h * step[0] + m * p.s.channels * static_cast<int>(sizeof(T)), v[h]);
-          if (p.q) keep(p, first + m * p.s.channels, v[h]);
-#pragma unroll
-          for (int k = 0; k < V; ++k) v[h][k] = inside ? v[h][k] * c[k] : 0.0f;
-          if (inside || p.zero_rest) store_v<T, V>(static_cast<T*>(p.out) + first + m * p.s.channels, v[h]);
-        }
-      }
   }
   __device__ bool wants_outside(const Args& p) const { return p.q || p.zero_rest; }
 };

@@ -52,8 +52,7 @@ constexpr int kMaxSlots = 16;
 constexpr int kMaxTileRows = 64;
 constexpr int kTileBytes = 36 * 1024;     // aim of a tile
 constexpr int kMaxStreams = 3;
-constexpr int kBlocksPerSm = 1;
-constexpr int kSmem = (227 / kBlocksPerSm - 1) * 1024;   // dynamic, for a block
+constexpr int kSmem = 226 * 1024;         // dynamic, of the 227 KB that a block can have
 
 // Division by a number known at launch, for n d below 2^32: a multiplication (an integer division takes
 // some 200 cycles, and most are on the way of the whole block).
@@ -465,7 +464,7 @@ __device__ __forceinline__ void gather(const Args& p, const Shared& sh, double* 
 }
 
 template <class Op, int V>
-__global__ void __launch_bounds__(kBlock, kBlocksPerSm) k_norm(const __grid_constant__ Args p) {
+__global__ void __launch_bounds__(kBlock, 1) k_norm(const __grid_constant__ Args p) {
   constexpr int Q = Op::Q, kStreams = Op::kStreams;
   extern __shared__ __align__(128) char smem[];
   __shared__ Shared sh;
@@ -701,22 +700,19 @@ __global__ void __launch_bounds__(kBlock, kBlocksPerSm) k_norm(const __grid_cons
   if (sh.abort) return;
 
   if constexpr (Op::kBackward) {
-    // dw and db: 8 sums at a time, the other threads of a sum take its blocks in turn
+    // dw and db: a warp to a sum, its lanes to the blocks
+    const int sums = Q * s.channels;
 #pragma unroll 1
-    for (int base = blockIdx.x * 8; base < Q * s.channels; base += gridDim.x * 8) {
-      const int i = base + (threadIdx.x & 7), k = threadIdx.x >> 3;
+    for (int i = blockIdx.x * kWarps + (threadIdx.x >> 5); i < sums; i += gridDim.x * kWarps) {
       double t = 0.0;
-      if (i < Q * s.channels)
-        for (int b = k; b < gridDim.x; b += kThreads / 8) t += p.chan[static_cast<size_t>(b) * Q * s.channels + i];
-      sum[threadIdx.x] = t;
-      meet_compute();
-      if (k == 0 && i < Q * s.channels) {
-        t = 0.0;
-        for (int j = 0; j < kThreads / 8; ++j) t += sum[j * 8 + threadIdx.x];
+#pragma unroll 4
+      for (int b = lane; b < gridDim.x; b += 32) t += p.chan[static_cast<size_t>(b) * sums + i];
+#pragma unroll
+      for (int o = 16; o > 0; o /= 2) t += __shfl_xor_sync(0xffffffffu, t, o);
+      if (lane == 0) {
         if (i < s.channels && p.grad_bias) p.grad_bias[i] = static_cast<float>(t);
         if (i >= s.channels && p.grad_weight) p.grad_weight[i - s.channels] = static_cast<float>(t);
       }
-      meet_compute();
     }
     if (!p.out) return;
   }
@@ -839,30 +835,24 @@ inline Shape shape_of(const Call& c, int width) {
 template <class Op, int V>
 etp_status launch(const Call& c, Args& p, const int (&row_bytes)[kMaxStreams], cudaStream_t stream, const char* what) {
   auto kernel = k_norm<Op, V>;
+  static thread_local int known_dev = -1, sms = 0;   // a device is asked once in a row
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess && dev != known_dev) {
+    e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    known_dev = e == cudaSuccess ? dev : -1;
+  }
+  if (e != cudaSuccess) return cuda_status(e, what);
   p.s = shape_of(c, V);
+  // A block for every rp rows at most, and no more blocks than run at once (one on an SM): the grid
+  // barrier needs them all on the device.
+  long long blocks = (static_cast<long long>(c.n_nodes) + p.s.rp - 1) / p.s.rp;
+  blocks = std::max(1LL, std::min(blocks, static_cast<long long>(std::min(sms, kMaxBlocks))));
   if (!plan_ring(p.s, Op::Q, Op::K * c.channels, Op::kAcc, row_bytes, &p.ring)) {
     set_error(std::string(what) + ": rows too long");
     return ETP_ERR_UNSUPPORTED;
   }
-  // what the device says about a kernel and a size of shared memory is asked for once in a row
-  static thread_local int known_dev = -1, known_bytes = 0, sms = 0, per_sm = 0;
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess && (dev != known_dev || p.ring.bytes != known_bytes)) {
-    e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kBlock, p.ring.bytes);
-    known_dev = e == cudaSuccess ? dev : -1;
-    known_bytes = p.ring.bytes;
-  }
-  if (e != cudaSuccess) return cuda_status(e, what);
-  // A block for every rp rows at most, and no more blocks than run at once: the grid barrier needs
-  // them all on the device.
-  long long blocks = (static_cast<long long>(c.n_nodes) + p.s.rp - 1) / p.s.rp;
-  long long resident = static_cast<long long>(per_sm) * sms;
-  if (resident > kMaxBlocks) resident = kMaxBlocks;
-  if (blocks > resident) blocks = resident;
-  if (blocks < 1) blocks = 1;
   p.s.rows = static_cast<int>((c.n_nodes + blocks - 1) / blocks);
   blocks = (static_cast<long long>(c.n_nodes) + p.s.rows - 1) / p.s.rows;
   auto tiles = [&](long long rows) { return static_cast<int>((rows + p.ring.tile_rows - 1) / p.ring.tile_rows); };
