@@ -562,8 +562,10 @@ def _norm_shape(shape, lmax, groups, node_ptr, weight, bias):
 
 def _norm_workspace(lmax, c, groups, s, backward, x, workspace):
     nb = group_norm_workspace_bytes(lmax, c, groups, s, backward)
-    if workspace is None or workspace.numel() < nb:
+    if workspace is None or workspace.numel() * workspace.element_size() < nb:
         workspace = x.new_empty(max(nb, 1), dtype=_torch().uint8)
+    elif workspace.get_device() != x.get_device():
+        raise ValueError(f"workspace on {workspace.device}, tensors on {x.device}")
     return workspace, nb
 
 

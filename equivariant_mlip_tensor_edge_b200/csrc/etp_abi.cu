@@ -880,6 +880,16 @@ size_t etp_group_norm_workspace_bytes(int lmax, int channels, int groups, int n_
   return norm::workspace_bytes(c, backward != 0);
 }
 
+static bool overlap(const void* a, const void* b, size_t bytes) {
+  const uintptr_t p = reinterpret_cast<uintptr_t>(a), q = reinterpret_cast<uintptr_t>(b);
+  return a && b && p < q + bytes && q < p + bytes;
+}
+
+// Bytes of the node rows of a call.
+static size_t row_bytes(const norm::Call& c) {
+  return static_cast<size_t>(c.n_nodes) * c.channels * (c.lmax + 1) * (c.lmax + 1) * (c.dtype == ETP_F32 ? 4 : 2);
+}
+
 // The checks that both directions of the group norm share.
 static etp_status check_norm(const char* who, const norm::Call& c, etp_ckpt_format format, bool backward,
                              const void* workspace, size_t workspace_bytes) {
@@ -930,6 +940,10 @@ etp_status etp_group_norm(int lmax, int channels, int groups, int n_nodes, int n
     set_error(std::string(who) + ": x, out and q must be 16-byte aligned");
     return ETP_ERR_INVALID_ARG;
   }
+  if (overlap(x, out, row_bytes(c))) {
+    set_error(std::string(who) + ": out may not overlap x");
+    return ETP_ERR_INVALID_ARG;
+  }
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (n_nodes == 0)
     return n_structs == 0 ? ETP_OK
@@ -958,6 +972,10 @@ etp_status etp_group_norm_backward(int lmax, int channels, int groups, int n_nod
   if ((format == ETP_CKPT_NONE && !aligned16(x)) || !aligned16(grad_out) || !aligned16(grad_x) ||
       (format != ETP_CKPT_NONE && (!aligned16(q) || !aligned16(scale)))) {
     set_error(std::string(who) + ": x, grad_out, grad_x, q and scale must be 16-byte aligned");
+    return ETP_ERR_INVALID_ARG;
+  }
+  if (overlap(grad_x, grad_out, row_bytes(c)) || (format == ETP_CKPT_NONE && overlap(grad_x, x, row_bytes(c)))) {
+    set_error(std::string(who) + ": grad_x may not overlap grad_out or x");
     return ETP_ERR_INVALID_ARG;
   }
   cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -878,6 +878,7 @@ etp_status launch(const Call& c, Args& p, const int (&row_bytes)[kMaxStreams], c
   const void* fn = reinterpret_cast<const void*>(kernel);
   if (blocks == 1) e = cudaLaunchKernel(fn, grid, block, args, p.ring.bytes, stream);
   else e = cudaLaunchCooperativeKernel(fn, grid, block, args, p.ring.bytes, stream);
+  if (e != cudaSuccess) cudaGetLastError();   // reported here, not by the next call
   return cuda_status(e, what);
 }
 

@@ -68,6 +68,7 @@ def test_library_refuses_bad_norm_arguments_before_device_work():
 
     def fwd(lmax=2, c=64, g=8, n=10, s=1, ptr=None, dtype=0, x=fake, eps=1e-5, act=1, out=fake, stats=fake, fmt=0,
             q=None, scale=None, ws=fake, nb=1 << 30):
+        out = ctypes.c_void_p(1 << 20) if out is fake else out
         return lib.etp_group_norm(lmax, c, g, n, s, ptr, dtype, x, None, None, eps, act, 0, out, stats, fmt, q, scale,
                                   ws, nb, None)
     for bad in (dict(lmax=4), dict(lmax=-1), dict(g=7), dict(g=0), dict(c=1028, g=1), dict(c=260, g=65),
@@ -81,10 +82,14 @@ def test_library_refuses_bad_norm_arguments_before_device_work():
         assert fwd(**bad) == 1, bad
         assert lib.etp_last_error().decode().startswith("etp_group_norm")
 
-    def bwd(n=10, s=1, ptr=None, x=fake, fmt=0, q=None, scale=None, stats=fake, go=fake, gx=fake, gw=fake, gb=fake,
-            nb=1 << 30):
+    def bwd(n=10, s=1, ptr=None, x=fake, fmt=0, q=None, scale=None, stats=fake, go=fake, gx=ctypes.c_void_p(1 << 20),
+            gw=fake, gb=fake, nb=1 << 30):
         return lib.etp_group_norm_backward(2, 64, 8, n, s, ptr, 0, x, fmt, q, scale, stats, None, None, 1, go, 0, gx,
                                            gw, gb, fake, nb, None)
+    other = ctypes.c_void_p(1 << 20)
+    assert fwd(out=ctypes.c_void_p(4096 + 16 * 64)) == 1 and "overlap" in lib.etp_last_error().decode()
+    assert bwd(gx=other, go=other) == 1 and "overlap" in lib.etp_last_error().decode()
+    assert bwd(gx=other, x=ctypes.c_void_p((1 << 20) - 64)) == 1
     for bad in (dict(gx=None, gw=None, gb=None), dict(x=None), dict(fmt=1), dict(go=None), dict(go=odd), dict(gx=odd),
                 dict(stats=None), dict(nb=nb)):
         assert bwd(**bad) == 1, bad
@@ -214,7 +219,8 @@ def _within(got, want, bound, what, most=np.inf):
 SHAPES = [(1, 0, 1, 1, "one"), (1, 2, 64, 8, "one"), (21, 2, 64, 8, "one"), (700, 1, 32, 4, "ragged"),
           (333, 3, 128, 16, "ragged"), (150, 2, 36, 3, "pad"), (90, 1, 50, 5, "rows"), (257, 0, 252, 7, "ragged"),
           (40, 3, 255, 5, "pad"), (64, 0, 1024, 64, "ragged"), (5000, 0, 8, 2, "ragged"), (3001, 2, 20, 5, "one"),
-          (2500, 1, 96, 3, "ragged"), (77, 1, 64, 64, "rows")]
+          (2500, 1, 96, 3, "ragged"), (77, 1, 64, 64, "rows"), (9, 1, 1024, 64, "ragged"), (31, 3, 256, 1, "pad"),
+          (11, 2, 454, 1, "one"), (12, 0, 512, 2, "rows")]
 
 
 @pytest.mark.gpu
@@ -263,6 +269,32 @@ def test_norm_backward(n, lmax, c, groups, kind, dtype, keep):
         _within(_np(a), e, t + 1e-30, what, info.max if dtype == "float16" and what == "grad_x" else np.inf)
     again = etp.group_norm_backward(ck if keep else xd, stats, wd, bd, g.to(DEV), lmax, groups, node_ptr, act)
     assert all(torch.equal(p, q) for p, q in zip(got, again))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("tail", ["ragged", "long"])
+def test_norm_of_more_rows_than_a_block_holds(tail):
+    """100 rows of 4 KB for each of 148 blocks, small structures among them, or one over the second half."""
+    n, lmax, c, groups = 14800, 3, 64, 8
+    x, w, b, g = _norm_inputs(n, lmax, c, "float32", 21)
+    ptr = _starts("ragged", n)
+    if tail == "long":
+        ptr = [p for p in ptr if p < n // 2] + [n]
+    node_ptr = torch.tensor(ptr, dtype=torch.int32, device=DEV)
+    xd, wd, bd = x.to(DEV), torch.from_numpy(w).to(DEV), torch.from_numpy(b).to(DEV)
+    out, stats, ck = etp.group_norm(xd, wd, bd, lmax, groups, node_ptr, checkpoint="int8")
+    want, st = norm64(_np(x), w, b, lmax, groups, ptr, 1e-5, "silu")
+    tiny = torch.finfo(torch.float32).smallest_normal
+    _within(_np(stats)[:, 1:], st[:, 1:], 16 * 2.0 ** -24 * st[:, 1:], "deviation")
+    _within(_np(out), want, norm_bounds(_np(x), w, b, lmax, groups, ptr, "silu", st, 0, tiny=tiny), "out")
+    alone = etp.checkpoint8(xd)
+    assert torch.equal(alone.scale, ck.scale) and torch.equal(alone.q, ck.q)
+    got = etp.group_norm_backward(ck, stats, wd, bd, g.to(DEV), lmax, groups, node_ptr)
+    kept, st = _np(ck.restore()), _np(stats)
+    want = norm64(kept, w, b, lmax, groups, ptr, 1e-5, "silu", grad=_np(g), stats=st)
+    bounds = norm_bounds(kept, w, b, lmax, groups, ptr, "silu", st, 0, grad=_np(g), tiny=tiny)
+    for a, e, t, what in zip(got, want, bounds, ("grad_x", "grad_weight", "grad_bias")):
+        _within(_np(a), e, t + 1e-30, what)
 
 
 @pytest.mark.gpu
@@ -370,12 +402,15 @@ def test_binding_checks_shapes_and_types():
                 lambda: etp.group_norm(x.double(), None, None, 1, 2),
                 lambda: etp.group_norm(x, None, None, 1, 2, out=torch.empty(6, 31, device=DEV)),
                 lambda: etp.group_norm(x, None, torch.ones(8), 1, 2),
+                lambda: etp.group_norm(x, None, None, 1, 2, workspace=torch.empty(1 << 22, dtype=torch.uint8)),
                 lambda: etp.group_norm_backward(x, stats, None, None, x.half(), 1, 2),
                 lambda: etp.group_norm_backward(x, stats[:, :2], None, None, x, 1, 2)):
         with pytest.raises(ValueError):
             bad()
-    with pytest.raises(etp.EtpError):
-        etp.group_norm(x, None, None, 1, 3)
+    for bad in (lambda: etp.group_norm(x, None, None, 1, 3), lambda: etp.group_norm(x, None, None, 1, 2, out=x),
+                lambda: etp.group_norm_backward(x, stats, None, None, x.clone(), 1, 2, grad_x=x)):
+        with pytest.raises(etp.EtpError):
+            bad()
 
 
 @pytest.mark.gpu
