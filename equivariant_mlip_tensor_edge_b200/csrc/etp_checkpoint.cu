@@ -118,7 +118,9 @@ void launch_vectors(bool int8, long long rows, int cols, int blocks, T* x, uint8
 
 // Any row length and alignment. A block takes a run of up to kUnit values, whole rows or a part of one
 // that starts at a block's first value, through shared memory: outside 16 bytes at a time, inside eight
-// values to a lane, one by one, as they are not aligned.
+// values to a lane, one by one, as they are not aligned. Bound by shared memory's banks and the
+// instructions of the single accesses: 16411 rows of 1153 bfloat16 stored and fetched in 63 us, 28 % of
+// the copy rate (a lane to a value: 90 us; single accesses to global memory: 123 us).
 constexpr int kUnit = 4096;
 
 struct Units {

@@ -13,7 +13,7 @@ struct Bwd {
   static constexpr int K = (L + 1) * (L + 1), Q = L + 2, kStreams = kKept ? 3 : 2;
   static constexpr bool kBackward = true;
   using Sum = float;
-  static constexpr int kRows = K == 1 ? 2 : 1;   // rows at once: loads in flight where a row has few
+  static constexpr int kRows = K == 1 ? 2 : 1;   // rows at once: more loads under way where a row has few
 
   static constexpr int kAcc = 4 * Q;
 

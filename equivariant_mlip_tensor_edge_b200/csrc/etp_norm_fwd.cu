@@ -12,7 +12,7 @@ struct Fwd {
   static constexpr int K = (L + 1) * (L + 1), Q = L + 2, kStreams = 1;
   static constexpr bool kBackward = false;
   using Sum = double;
-  static constexpr int kRows = K == 1 ? 4 : K == 4 ? 2 : 1;   // rows at once: loads in flight where a row has few
+  static constexpr int kRows = K == 1 ? 4 : K == 4 ? 2 : 1;   // rows at once: more loads under way where a row has few
   static constexpr int kLanes = kCkptBlock / V;   // threads that share a checkpoint block
 
   static constexpr int kAcc = 16 + 4 * L;         // bytes of a thread's sums: two of 64 bits, L of 32
