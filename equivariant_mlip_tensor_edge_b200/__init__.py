@@ -100,6 +100,7 @@ def _check(status, where):
         raise EtpError(status, where)
 
 
+@functools.lru_cache(maxsize=None)
 def _torch():
     import torch
     return torch
@@ -413,19 +414,21 @@ _DTYPE_CODES = {}
 
 
 def _dtype_code(dtype):
-    if not _DTYPE_CODES:
+    code = _DTYPE_CODES.get(dtype)
+    if code is None and not _DTYPE_CODES:
         torch = _torch()
         _DTYPE_CODES.update({torch.float32: 0, torch.bfloat16: 1, torch.float16: 2})
-    code = _DTYPE_CODES.get(dtype)
+        code = _DTYPE_CODES.get(dtype)
     if code is None:
         raise ValueError(f"float32, bfloat16 or float16 values expected, got {dtype}")
     return code
 
 
 def _named(table, name, what):
-    if name not in table:
+    code = table.get(name)
+    if code is None:
         raise ValueError(f"{what} must be one of {[k for k in table if k]} or None, got {name!r}")
-    return table[name]
+    return code
 
 
 def _rows(t):
@@ -486,24 +489,27 @@ class Checkpoint8:
         return self.q.numel() + self.scale.numel()
 
     def _checked(self):
+        """(format code, codes, scales) for the library."""
         torch = _torch()
-        _one_device(self.q, self.scale)
-        cols = self.q.shape[-1]
-        if self.q.dtype not in (torch.int8, torch.float8_e4m3fn) or self.scale.dtype != torch.uint8:
+        q, scale = self.q, self.scale
+        fmt = 1 if q.dtype == torch.int8 else 2 if q.dtype == torch.float8_e4m3fn else 0
+        if fmt == 0 or scale.dtype != torch.uint8:
             raise ValueError("a checkpoint has int8 or float8_e4m3fn codes and uint8 scales")
-        if self.scale.shape != self.q.shape[:-1] + (-(-cols // CKPT_BLOCK),):
-            raise ValueError(f"scales of shape {tuple(self.scale.shape)} do not fit codes of shape {tuple(self.q.shape)}")
-        return _rows(self.q), _rows(self.scale)
+        shape = q.shape
+        if scale.shape != shape[:-1] + (-(-shape[-1] // CKPT_BLOCK),):
+            raise ValueError(f"scales of shape {tuple(scale.shape)} do not fit codes of shape {tuple(shape)}")
+        return fmt, _rows(q), _rows(scale)
 
     def restore(self, dtype=None, out=None):
         """The values the checkpoint stands for, in ``dtype`` (default: that of the activations)."""
-        q, scale = self._checked()
+        fmt, q, scale = self._checked()
+        shape = q.shape
         if out is None:
-            out = q.new_empty(q.shape, dtype=dtype or self.dtype)
-        elif out.shape != q.shape or not out.is_contiguous() or (dtype is not None and out.dtype != dtype):
+            out = q.new_empty(shape, dtype=dtype or self.dtype)
+        elif out.shape != shape or not out.is_contiguous() or (dtype is not None and out.dtype != dtype):
             raise ValueError("out must be contiguous, of the checkpoint's shape and the dtype asked for")
-        cols = q.shape[-1]
-        _call(_one_device(q, out), "etp_checkpoint_restore", load_library().etp_checkpoint_restore, CKPT_FORMATS[self.format],
+        cols = shape[-1]
+        _call(_one_device(q, scale, out), "etp_checkpoint_restore", load_library().etp_checkpoint_restore, fmt,
               _dtype_code(out.dtype), q.numel() // max(cols, 1), cols, q.data_ptr(), scale.data_ptr(), out.data_ptr())
         return out
 
@@ -553,9 +559,9 @@ def _norm_shape(shape, lmax, groups, node_ptr, weight, bias):
     c = dim // comps
     if node_ptr is not None and (node_ptr.dim() != 1 or node_ptr.numel() < 1):
         raise ValueError("node_ptr is a vector of n_structs + 1 row numbers")
-    if weight is not None and tuple(weight.shape) != (lmax + 1, c):
+    if weight is not None and weight.shape != (lmax + 1, c):
         raise ValueError(f"weight must be [{lmax + 1}, {c}], got {tuple(weight.shape)}")
-    if bias is not None and tuple(bias.shape) != (c,):
+    if bias is not None and bias.shape != (c,):
         raise ValueError(f"bias must be [{c}], got {tuple(bias.shape)}")
     return n, c, 1 if node_ptr is None else node_ptr.numel() - 1
 
@@ -623,14 +629,14 @@ def group_norm_backward(x, stats, weight, bias, grad_out, lmax, groups, node_ptr
     act = _named(ACTIVATIONS, activation, "activation")
     if grad_out.shape != x.shape or (not kept and grad_out.dtype != x.dtype):
         raise ValueError(f"grad_out must have x's shape and type, got {tuple(grad_out.shape)} {grad_out.dtype}")
-    if tuple(stats.shape) != (s, lmax + 2, groups):
+    if stats.shape != (s, lmax + 2, groups):
         raise ValueError(f"stats must be [{s}, {lmax + 2}, {groups}], got {tuple(stats.shape)}")
     if not (want_grad_x or want_grad_affine):
         return None, None, None
     grad_out, stats = _rows(grad_out), _f32(stats)
-    q = scale = None
+    fmt, q, scale = x._checked() if kept else (0, None, None)
     if kept:
-        q, scale = x._checked()
+        _one_device(grad_out, scale)
     else:
         x = _rows(x)
     weight = None if weight is None else _f32(weight)
@@ -643,7 +649,7 @@ def group_norm_backward(x, stats, weight, bias, grad_out, lmax, groups, node_ptr
     gb = grad_out.new_empty(c, dtype=_torch().float32) if want_grad_affine else None
     ws, nb = _norm_workspace(lmax, c, groups, s, True, grad_out, workspace)
     _call(index, "etp_group_norm_backward", load_library().etp_group_norm_backward, lmax, c, groups, n, s,
-          _addr(node_ptr), dtype, None if kept else x.data_ptr(), CKPT_FORMATS[x.format] if kept else 0, _addr(q),
+          _addr(node_ptr), dtype, None if kept else x.data_ptr(), fmt, _addr(q),
           _addr(scale), stats.data_ptr(), _addr(weight), _addr(bias), act, grad_out.data_ptr(), made,
           grad_x.data_ptr() if want_grad_x else None, _addr(gw), _addr(gb), ws.data_ptr(), nb)
     return (grad_x if want_grad_x else None), gw, gb
