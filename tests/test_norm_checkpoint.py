@@ -574,3 +574,19 @@ def test_half_precision_rows_through_autograd():
     want = etp.group_norm_backward(ck, st, wr.detach(), br.detach(), g.to(DEV), 1, 4)
     assert xr.grad.dtype == torch.bfloat16
     assert all(torch.equal(p.grad, q) for p, q in zip((xr, wr, br), want))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("keep", [None, "int8"])
+def test_broadcast_cotangent_and_partial_leaves(keep):
+    """sum() hands down an expanded cotangent; leaves that need no gradient get none."""
+    x, w, b, _ = _norm_inputs(40, 1, 24, "float32", 14)
+    xd, wd, bd = x.to(DEV), torch.from_numpy(w).to(DEV), torch.from_numpy(b).to(DEV)
+    fn = etp.group_norm_function(keep)
+    y, st, ck = etp.group_norm(xd, wd, bd, 1, 3, checkpoint=keep)
+    want = etp.group_norm_backward(ck if keep else xd, st, wd, bd, torch.ones_like(y), 1, 3)
+    for needs in ((True, True, True), (True, False, False), (False, True, False), (False, False, True)):
+        leaves = [t.clone().requires_grad_(n) for t, n in zip((xd, wd, bd), needs)]
+        fn.apply(*leaves, 1, 3).sum().backward()
+        for leaf, grad, n in zip(leaves, want, needs):
+            assert torch.equal(leaf.grad, grad) if n else leaf.grad is None
