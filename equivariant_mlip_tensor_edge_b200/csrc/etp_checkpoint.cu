@@ -117,11 +117,12 @@ void launch_vectors(bool int8, long long rows, int cols, int blocks, T* x, uint8
 }
 
 // Any row length and alignment. A block takes a run of up to kUnit values, whole rows or a part of one
-// that starts at a block's first value, through shared memory: outside 16 bytes at a time, inside eight
-// values to a lane, one by one, as they are not aligned. Bound by shared memory's banks and the
-// instructions of the single accesses: 16411 rows of 1153 bfloat16 stored and fetched in 63 us, 28 % of
-// the copy rate (a lane to a value: 90 us; single accesses to global memory: 123 us).
-constexpr int kUnit = 4096;
+// that starts at a block's first value, through shared memory: outside 16 bytes at a time, inside value by
+// value, as they are not aligned. Bound by the instructions of the single accesses and, between a
+// unit's arrival and its leaving, by how many blocks an SM has under way: 16411 rows of 1153 bfloat16
+// stored and fetched in 48 us, 37 % of the copy rate (units of 4096 values and 256 threads: 64 us; a lane
+// to a value: 90 us; single accesses to global memory: 123 us).
+constexpr int kUnit = 6144, kUnitThreads = 128;
 
 struct Units {
   long long n, rows;
@@ -136,7 +137,7 @@ __device__ __forceinline__ void move_bytes(char* shared, char* global, int n) {
   const int off = static_cast<int>(reinterpret_cast<uintptr_t>(global) & 15u), head = min((16 - off) & 15, n);
   const int body = (n - head) >> 4, tail = n - head - (body << 4);
   char* s = shared + off;
-  for (int i = threadIdx.x; i < body; i += kThreads) {
+  for (int i = threadIdx.x; i < body; i += kUnitThreads) {
     uint4* g = reinterpret_cast<uint4*>(global + head) + i;
     uint4* t = reinterpret_cast<uint4*>(s + head) + i;
     if (kIn) *t = __ldcs(g);
@@ -150,7 +151,7 @@ __device__ __forceinline__ void move_bytes(char* shared, char* global, int n) {
 }
 
 template <class T, bool kStore, bool kInt8, int kLanes>
-__global__ void __launch_bounds__(kThreads, 4) k_units(Units p, T* x, uint8_t* q, uint8_t* scale) {
+__global__ void __launch_bounds__(kUnitThreads, 6) k_units(Units p, T* x, uint8_t* q, uint8_t* scale) {
   __shared__ __align__(16) char values[kUnit * sizeof(T) + 16];
   __shared__ __align__(16) char codes[kUnit + 32];
   __shared__ __align__(16) char scales[kUnit + 16];
@@ -175,55 +176,66 @@ __global__ void __launch_bounds__(kThreads, 4) k_units(Units p, T* x, uint8_t* q
       move_bytes<true>(scales, reinterpret_cast<char*>(gs), items);
     }
     __syncthreads();
-    const int end = (items + per_warp - 1) / per_warp;
-    for (int it = threadIdx.x >> 5; it < end; it += kThreads / 32) {
-      const int b = it * per_warp + first;
-      const int r = p.per_row > 1 ? 0 : p.blocks_m ? static_cast<int>(__umulhi(b, p.blocks_m)) : b;
-      const int col = (b - r * blocks) * kCkptBlock + in_block * 8, at = r * nc + col;
-      const int count = b < items ? min(max(nc - col, 0), 8) : 0;
-      float v[8];
+    // Two blocks to a lane, 4 values of each (or one short row of at most 4 to each): 4 lanes' values in
+    // 32 bytes keep the accesses of a warp at two a bank.
+    const int end = (items + 2 * per_warp - 1) / (2 * per_warp);
+    for (int it = threadIdx.x >> 5; it < end; it += kUnitThreads / 32) {
+      int at[2], count[2];
+      float v[2][4];
+      unsigned codes4[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int b = (it * 2 + h) * per_warp + first;
+        const int r = p.per_row > 1 ? 0 : p.blocks_m ? static_cast<int>(__umulhi(b, p.blocks_m)) : b;
+        const int col = (b - r * blocks) * kCkptBlock + in_block * 4;
+        at[h] = r * nc + col;
+        count[h] = b < items ? min(max(nc - col, 0), 4) : 0;
+        if (kStore) {
+          if (count[h] == 4) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[h][k] = to_f32<T>(sx[at[h] + k]);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[h][k] = k < count[h] ? to_f32<T>(sx[at[h] + k]) : 0.0f;
+          }
+        } else if (count[h] > 0) {
+          // what stands behind the last value of a row is the next one's, or room in shared memory
+          const uint8_t* from = sq + at[h];
+          codes4[h] = from[0] | from[1] << 8 | from[2] << 16 | static_cast<unsigned>(from[3]) << 24;
+          decode4(codes4[h], scale_of(ss[b]), kInt8, v[h]);
+        }
+      }
       if (kStore) {
-        if (count == 8) {
+        float m[2];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) v[k] = to_f32<T>(sx[at + k]);
-        } else {
+        for (int h = 0; h < 2; ++h) m[h] = max_abs(max_abs(v[h][0], v[h][1]), max_abs(v[h][2], v[h][3]));
 #pragma unroll
-          for (int k = 0; k < 8; ++k) v[k] = k < count ? to_f32<T>(sx[at + k]) : 0.0f;
-        }
-        float m = max_abs(max_abs(max_abs(v[0], v[1]), max_abs(v[2], v[3])), max_abs(max_abs(v[4], v[5]), max_abs(v[6], v[7])));
+        for (int o = 1; o < kLanes; o *= 2)
 #pragma unroll
-        for (int o = 1; o < kLanes; o *= 2) m = max_abs(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const unsigned byte = scale_byte(m, kInt8);
-        const float inv = inv_scale(byte);
-        const float lo[4] = {v[0], v[1], v[2], v[3]}, hi[4] = {v[4], v[5], v[6], v[7]};
-        const unsigned t[2] = {encode4(lo, inv, byte == kCkptBad, kInt8), encode4(hi, inv, byte == kCkptBad, kInt8)};
-        if (count == 8) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k) sq[at + k] = static_cast<uint8_t>(t[k / 4] >> (8 * (k & 3)));
-        } else {
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            if (k < count) sq[at + k] = static_cast<uint8_t>(t[k / 4] >> (8 * (k & 3)));
-        }
-        if (in_block == 0 && b < items) ss[b] = static_cast<uint8_t>(byte);
-      } else if (count > 0) {
-        // what stands behind the last value of a row is the next one's, or room in shared memory
-        const float scale_b = scale_of(ss[b]);
+          for (int h = 0; h < 2; ++h) m[h] = max_abs(m[h], __shfl_xor_sync(0xffffffffu, m[h], o));
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const uint8_t* from = sq + at + 4 * h;
-          float w[4];
-          decode4(from[0] | from[1] << 8 | from[2] << 16 | static_cast<unsigned>(from[3]) << 24, scale_b, kInt8, w);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) v[4 * h + k] = held<T>(w[k]);
+          const unsigned byte = scale_byte(m[h], kInt8);
+          codes4[h] = encode4(v[h], inv_scale(byte), byte == kCkptBad, kInt8);
+          const int b = (it * 2 + h) * per_warp + first;
+          if (in_block == 0 && b < items) ss[b] = static_cast<uint8_t>(byte);
         }
-        if (count == 8) {
+      }
 #pragma unroll
-          for (int k = 0; k < 8; ++k) sx[at + k] = from_f32<T>(v[k]);
+      for (int h = 0; h < 2; ++h) {
+        if (count[h] == 4) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            if (kStore) sq[at[h] + k] = static_cast<uint8_t>(codes4[h] >> (8 * k));
+            else sx[at[h] + k] = from_f32<T>(held<T>(v[h][k]));
+          }
         } else {
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            if (k < count) sx[at + k] = from_f32<T>(v[k]);
+          for (int k = 0; k < 3; ++k) {
+            if (k >= count[h]) continue;
+            if (kStore) sq[at[h] + k] = static_cast<uint8_t>(codes4[h] >> (8 * k));
+            else sx[at[h] + k] = from_f32<T>(held<T>(v[h][k]));
+          }
         }
       }
     }
@@ -249,10 +261,10 @@ void launch_units(bool int8, long long rows, int cols, int blocks, T* x, uint8_t
   p.unit_rows = p.per_row > 1 ? 1 : kUnit / cols;
   p.n = (rows + p.unit_rows - 1) / p.unit_rows * p.per_row;
   p.blocks_m = blocks > 1 ? static_cast<unsigned>(((1ULL << 32) + blocks - 1) / blocks) : 0u;
-  const int grid = static_cast<int>(std::min<long long>(p.n, 148 * 8));
-  auto run = [&](auto kernel) { kernel<<<grid, kThreads, 0, s>>>(p, x, q, scale); };
-  if (int8) cols > 8 ? run(k_units<T, kStore, true, 4>) : run(k_units<T, kStore, true, 1>);
-  else cols > 8 ? run(k_units<T, kStore, false, 4>) : run(k_units<T, kStore, false, 1>);
+  const int grid = static_cast<int>(std::min<long long>(p.n, 148 * 16));
+  auto run = [&](auto kernel) { kernel<<<grid, kUnitThreads, 0, s>>>(p, x, q, scale); };
+  if (int8) cols > 4 ? run(k_units<T, kStore, true, 8>) : run(k_units<T, kStore, true, 1>);
+  else cols > 4 ? run(k_units<T, kStore, false, 8>) : run(k_units<T, kStore, false, 1>);
 }
 
 bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }

@@ -143,7 +143,8 @@ def _awkward(rows, cols, dtype, seed):
 @pytest.mark.gpu
 @pytest.mark.parametrize("fmt", ["int8", "e4m3"])
 @pytest.mark.parametrize("dtype", list(TYPES))
-@pytest.mark.parametrize("rows,cols", [(1, 1), (9, 31), (13, 32), (8, 33), (40, 576), (11, 100), (300, 2048)])
+@pytest.mark.parametrize("rows,cols", [(1, 1), (9, 31), (13, 32), (8, 33), (40, 576), (11, 100), (300, 2048), (700, 3),
+                                       (40, 5), (9, 17), (9, 20011)])
 def test_checkpoint_is_exact(rows, cols, dtype, fmt):
     x = _awkward(rows, cols, dtype, rows + cols)
     ck = etp.checkpoint8(x.to(DEV), fmt)
