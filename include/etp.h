@@ -294,7 +294,7 @@ etp_status etp_forces(int n_nodes, int n_edges, const int* row_ptr, const int* t
  * smallest integer >= -126 with max|x| <= 127 2^e (ETP_CKPT_INT8) or 448 2^e (ETP_CKPT_E4M3); q is
  * x / 2^e rounded to the nearest integer or e4m3 number, ties to even; the scale byte is e + 127.
  * A run with a NaN or an infinity gets scale byte 255 and codes 0. x: dtype values, aligned to their
- * size; q is faster when 4-byte aligned with x 16-byte aligned. Device pointers; asynchronous. */
+ * size; fastest with cols % 4 == 0, x aligned to 4 values and q to 4 bytes. Device pointers; asynchronous. */
 etp_status etp_checkpoint_store(etp_ckpt_format format, etp_dtype dtype, long long rows, int cols, const void* x,
                                 void* q, void* scale, void* stream);
 
@@ -323,10 +323,11 @@ size_t etp_group_norm_workspace_bytes(int lmax, int channels, int groups, int n_
  * they were in out, or zeroed if zero_rest is nonzero. format: ETP_CKPT_NONE, or the checkpoint of all
  * rows of x is stored to q and scale as by etp_checkpoint_store (q 16-byte aligned), in the same
  * pass when channels % 32 == 0. lmax 0..3; channels / groups whole, groups <= 64, dim <= 4096, channels
- * <= 1024, 512 or 256 as channels / groups is a multiple of 4, of 2 or odd; eps >= 0. Sums are 64-bit; equal
- * calls give equal bits. Asynchronous (a cooperative launch); concurrent calls need their own
- * workspace, 256-byte aligned. With ETP_VALIDATE=1 node_ptr is checked first (ETP_ERR_BAD_GRAPH), and
- * the call waits and returns ETP_ERR_CUDA if a bounded pipeline wait gave up. */
+ * <= 1024, 512 or 256 as channels / groups is a multiple of 4, of 2 or odd; eps >= 0. Sums are taken
+ * in 64 bits where they cancel or join threads, else in 32; equal calls give equal bits. Asynchronous
+ * (a cooperative launch); concurrent calls need a workspace each, 256-byte aligned. With ETP_VALIDATE=1
+ * node_ptr is checked first (ETP_ERR_BAD_GRAPH), and the call waits and returns ETP_ERR_CUDA if a
+ * bounded pipeline wait gave up. */
 etp_status etp_group_norm(int lmax, int channels, int groups, int n_nodes, int n_structs, const int* node_ptr,
                           etp_dtype dtype, const void* x, const float* weight, const float* bias, float eps,
                           etp_activation activation, int zero_rest, void* out, float* stats, etp_ckpt_format format,
