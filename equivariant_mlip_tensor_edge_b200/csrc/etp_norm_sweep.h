@@ -248,30 +248,46 @@ __device__ __forceinline__ void bulk_g2s_once(void* dst, const void* src, uint32
                : "memory");
 }
 
-// Starts a tile's copies into its slot, a lane to a stream: the aligned bytes around the tile, and by
-// hand the last bytes of an array that do not fill 16. once: it will not be found in L2 again.
+// Bytes that rows [t0, t1) of an array of n_rows rows take: [a, b) by a bulk copy, in whole units of 16, and
+// [b, e), if any, by hand: bytes of the array behind its last whole unit.
+struct TileBytes {
+  size_t a, b, e;
+};
+__host__ __device__ inline TileBytes tile_bytes(int t0, int t1, int n_rows, int row_bytes) {
+  const size_t unit = 15, rb = static_cast<size_t>(row_bytes), whole = (n_rows * rb) & ~unit;
+  TileBytes t;
+  t.a = (t0 * rb) & ~unit;
+  t.e = t1 * rb;
+  t.b = (t.e + unit) & ~unit;
+  if (t.b > whole) t.b = whole;
+  if (t.b < t.a) t.b = t.a;
+  return t;
+}
+// Whether that can leave bytes to copy by hand: not with 16 rows or more behind the tile.
+__host__ __device__ inline bool near_end(int t1, int n_rows) { return n_rows - t1 < 16; }
+
+// Starts a tile's copies into its slot, a lane to a stream, and does those by hand. once: it will not be
+// found in L2 again.
 template <int kStreams>
 __device__ __forceinline__ void copy_tile(const Args& p, Shared* sh, char* smem, int slot, int t0, int t1, bool once) {
   const Ring& ring = p.ring;
   const int lane = threadIdx.x & 31;
   char* dst = smem + ring.o_ring + static_cast<size_t>(slot) * ring.slot_bytes;
   if (lane < kStreams) {
-    const size_t rb = ring.row_bytes[lane], e = t1 * rb, a = (t0 * rb) & ~static_cast<size_t>(15);
-    const size_t whole = (p.s.n_nodes * rb) & ~static_cast<size_t>(15);
-    const size_t b = max(a, min((e + 15) & ~static_cast<size_t>(15), whole));
-    const uint32_t bytes = static_cast<uint32_t>(b - a);
+    const TileBytes t = tile_bytes(t0, t1, p.s.n_nodes, ring.row_bytes[lane]);
+    const uint32_t bytes = static_cast<uint32_t>(t.b - t.a);
     tc::mbar_expect_tx(&sh->full[slot], bytes);
-    if (bytes && once) bulk_g2s_once(dst + ring.off[lane], ring.src[lane] + a, bytes, &sh->full[slot]);
-    else if (bytes) tc::bulk_g2s(dst + ring.off[lane], ring.src[lane] + a, bytes, &sh->full[slot]);
+    if (bytes && once) bulk_g2s_once(dst + ring.off[lane], ring.src[lane] + t.a, bytes, &sh->full[slot]);
+    else if (bytes) tc::bulk_g2s(dst + ring.off[lane], ring.src[lane] + t.a, bytes, &sh->full[slot]);
     if (lane == 0) ++sh->copies[slot];
   }
-  if (t1 == p.s.n_nodes) {
+  if (near_end(t1, p.s.n_nodes)) {
 #pragma unroll
     for (int k = 0; k < kStreams; ++k) {
-      const size_t rb = ring.row_bytes[k], e = t1 * rb, a = (t0 * rb) & ~static_cast<size_t>(15);
-      const size_t b = max(a, e & ~static_cast<size_t>(15));
-      if (b + lane < e) dst[ring.off[k] + (b - a) + lane] = ring.src[k][b + lane];
+      const TileBytes t = tile_bytes(t0, t1, p.s.n_nodes, ring.row_bytes[k]);
+      if (t.b + lane < t.e) dst[ring.off[k] + (t.b - t.a) + lane] = ring.src[k][t.b + lane];
     }
+    tc::fence_proxy_async();   // before a later bulk copy into the same bytes
   }
 }
 
@@ -857,6 +873,24 @@ inline Shape shape_of(const Call& c, int width) {
   return s;
 }
 
+// Shape, shared memory and number of blocks of a call on a device of `sms` SMs; false: rows too long.
+inline bool plan_call(const Call& c, int width, int q, int dim, int acc_thread, const int (&row_bytes)[kMaxStreams],
+                      int sms, Shape* s, Ring* ring, long long* blocks) {
+  *s = shape_of(c, width);
+  if (!plan_ring(*s, q, dim, acc_thread, row_bytes, ring)) return false;
+  // A block for every rp rows at most, and no more blocks than run at once (one on an SM): the grid
+  // barrier needs them all on the device.
+  const long long n = c.n_nodes, most = std::min(sms, kMaxBlocks);
+  *blocks = std::max(1LL, std::min((n + s->rp - 1) / s->rp, most));
+  s->rows = static_cast<int>((n + *blocks - 1) / *blocks);
+  *blocks = (n + s->rows - 1) / s->rows;
+  auto tiles = [&](long long rows) { return static_cast<int>((rows + ring->tile_rows - 1) / ring->tile_rows); };
+  ring->tiles = tiles(s->rows);
+  ring->tiles_last = tiles(n - (*blocks - 1) * s->rows);
+  ring->l2_tiles = static_cast<int>(kL2Bytes / *blocks / ring->slot_bytes);
+  return true;
+}
+
 template <class Op, int V>
 etp_status launch(const Call& c, Args& p, const int (&row_bytes)[kMaxStreams], cudaStream_t stream, const char* what) {
   auto kernel = k_norm<Op, V>;
@@ -869,21 +903,11 @@ etp_status launch(const Call& c, Args& p, const int (&row_bytes)[kMaxStreams], c
     known_dev = e == cudaSuccess ? dev : -1;
   }
   if (e != cudaSuccess) return cuda_status(e, what);
-  p.s = shape_of(c, V);
-  // A block for every rp rows at most, and no more blocks than run at once (one on an SM): the grid
-  // barrier needs them all on the device.
-  long long blocks = (static_cast<long long>(c.n_nodes) + p.s.rp - 1) / p.s.rp;
-  blocks = std::max(1LL, std::min(blocks, static_cast<long long>(std::min(sms, kMaxBlocks))));
-  if (!plan_ring(p.s, Op::Q, Op::K * c.channels, Op::kAcc, row_bytes, &p.ring)) {
+  long long blocks = 0;
+  if (!plan_call(c, V, Op::Q, Op::K * c.channels, Op::kAcc, row_bytes, sms, &p.s, &p.ring, &blocks)) {
     set_error(std::string(what) + ": rows too long");
     return ETP_ERR_UNSUPPORTED;
   }
-  p.s.rows = static_cast<int>((c.n_nodes + blocks - 1) / blocks);
-  blocks = (static_cast<long long>(c.n_nodes) + p.s.rows - 1) / p.s.rows;
-  auto tiles = [&](long long rows) { return static_cast<int>((rows + p.ring.tile_rows - 1) / p.ring.tile_rows); };
-  p.ring.tiles = tiles(p.s.rows);
-  p.ring.l2_tiles = static_cast<int>(kL2Bytes / blocks / p.ring.slot_bytes);
-  p.ring.tiles_last = tiles(c.n_nodes - (blocks - 1) * p.s.rows);
   void* args[] = {&p};
   const dim3 grid(static_cast<unsigned>(blocks)), block(kBlock);
   const void* fn = reinterpret_cast<const void*>(kernel);

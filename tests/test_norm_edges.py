@@ -1,0 +1,62 @@
+"""Group norm and 8-bit checkpoints where sizes, ranges and arguments end: the launch plan replayed on the
+CPU, refusals, and kernels against float64 on the GPU."""
+import os
+import shutil
+import subprocess
+
+import pytest
+
+from tests._norm_side import keep64, norm64, norm_bounds
+from tests.test_norm_checkpoint import DEV, TYPES, _norm_inputs, _np, _starts, _within, etp, torch
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
+
+
+# ------------------------------------------------------------------ bytes of a tile
+
+@pytest.mark.skipif(shutil.which(NVCC) is None, reason="no nvcc")
+def test_plan_brings_every_byte_of_every_tile(tmp_path):
+    """The launch plan over many shapes and row counts, on the host: each tile's bytes are copied, in bulk or
+    by hand, within the array and the slot."""
+    exe = tmp_path / "norm_plan"
+    csrc = os.path.join(ROOT, "equivariant_mlip_tensor_edge_b200", "csrc")
+    subprocess.run([NVCC, "-std=c++17", "-O1", "-gencode", "arch=compute_100a,code=sm_100a", "-I" + os.path.join(ROOT, "include"),
+                    "-I" + csrc, os.path.join(ROOT, "tests", "c", "norm_plan.cu"), "-o", str(exe)],
+                   check=True, capture_output=True, text=True)
+    run = subprocess.run([str(exe)], capture_output=True, text=True, timeout=300)
+    assert run.returncode == 0 and run.stdout.strip().endswith(" 0 wrong"), run.stdout + run.stderr
+
+
+def _check_forward(x, w, b, lmax, groups, ptr, act, out, stats, dtype):
+    want, st = norm64(_np(x), w, b, lmax, groups, ptr, 1e-5, act)
+    info = torch.finfo(TYPES[dtype])
+    _within(_np(stats)[:, 1:], st[:, 1:], 16 * 2.0 ** -24 * st[:, 1:], "deviation")
+    _within(_np(out), want, norm_bounds(_np(x), w, b, lmax, groups, ptr, act, st, info.eps if dtype != "float32" else 0,
+                                        tiny=info.smallest_normal), "out")
+
+
+def _check_backward(xin, w, b, g, lmax, groups, ptr, act, stats, got, dtype):
+    st, info = _np(stats), torch.finfo(TYPES[dtype])
+    want = norm64(xin, w, b, lmax, groups, ptr, 1e-5, act, grad=_np(g), stats=st)
+    bounds = norm_bounds(xin, w, b, lmax, groups, ptr, act, st, info.eps if dtype != "float32" else 0, grad=_np(g),
+                         tiny=info.smallest_normal)
+    for a, e, t, what in zip(got, want, bounds, ("grad_x", "grad_weight", "grad_bias")):
+        _within(_np(a), e, t + 1e-30, what, info.max if dtype == "float16" and what == "grad_x" else float("inf"))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("keep", [None, "int8", "e4m3"])
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("n,lmax,c,groups", [(871, 2, 32, 4), (931, 1, 32, 4), (198, 0, 64, 8), (514, 0, 1, 1), (519, 0, 1, 1)])
+def test_short_rows_at_the_end_of_the_array(n, lmax, c, groups, dtype, keep):
+    """Fewer than 16 bytes of an array behind a tile that is not the last: rows (or rows of scales) of
+    under 16 bytes, a block's border a row or a few before the end."""
+    x, w, b, g = _norm_inputs(n, lmax, c, dtype, n)
+    ptr = _starts("ragged", n)
+    xd, wd, bd = x.to(DEV), torch.from_numpy(w).to(DEV), torch.from_numpy(b).to(DEV)
+    node_ptr = torch.tensor(ptr, dtype=torch.int32, device=DEV)
+    out, stats, ck = etp.group_norm(xd, wd, bd, lmax, groups, node_ptr, checkpoint=keep)
+    _check_forward(x, w, b, lmax, groups, ptr, "silu", out, stats, dtype)
+    got = etp.group_norm_backward(ck if keep else xd, stats, wd, bd, g.to(DEV), lmax, groups, node_ptr)
+    _check_backward(keep64(_np(x), keep)[0] if keep else _np(x), w, b, g, lmax, groups, ptr, "silu", stats, got, dtype)
