@@ -518,7 +518,10 @@ __global__ void __launch_bounds__(kBlock, 1) k_norm(const __grid_constant__ Args
   w.tiles = blockIdx.x == gridDim.x - 1 ? ring.tiles_last : ring.tiles;
   const int held = min(w.tiles, ring.slots), last_once = w.tiles - ring.slots - ring.l2_tiles;
 
-  if (threadIdx.x >= kThreads) {   // the copying warp
+  // The last warp copies, the others compute. All of them meet at the same three places: before the first
+  // sweep, behind it, and at the grid barrier.
+  const bool copies = threadIdx.x >= kThreads;
+  if (copies) {
     if (lane < ring.slots) {
       tc::mbar_init(&sh.full[lane], kStreams + 1);
       tc::mbar_init(&sh.empty[lane], kWarps);
@@ -536,46 +539,6 @@ __global__ void __launch_bounds__(kBlock, 1) k_norm(const __grid_constant__ Args
       const int t0 = w.r0 + k * ring.tile_rows;
       copy_tile<kStreams>(p, &sh, smem, k, t0, min(t0 + ring.tile_rows, w.r1), k < last_once);
     }
-    __syncthreads();
-    Seen seen;
-    Phases freed;
-    bool ok = true;
-    int slot = 0, place = 0;
-#pragma unroll 1
-    for (int k = 0; k < w.tiles; ++k) {
-      const int t0 = w.r0 + k * ring.tile_rows, t1 = min(t0 + ring.tile_rows, w.r1);
-      if (k >= held) {
-        ok = tc::warp_wait(&sh.empty[slot], freed.of(slot), &sh.abort, p.err, 1);
-        if (!ok) break;
-        freed.pass(slot);
-        copy_tile<kStreams>(p, &sh, smem, slot, t0, t1, k < last_once);
-      }
-      describe_tile(p, w, &sh, smem, slot, t0, t1, place, &seen);
-      if (++slot == ring.slots) slot = 0;
-      if ((place += ring.tile_rows) >= ring.acc_rows) place -= ring.acc_rows;
-    }
-    __syncthreads();
-    if (gridDim.x > 1) cg::this_grid().sync();
-    if (p.out && ok) {
-      // down again, from the slot of the last tile that the ring lost
-      seen = Seen();
-      if (held == ring.slots && --slot < 0) slot = ring.slots - 1;
-#pragma unroll 1
-      for (int k = w.tiles - held - 1; k >= 0; --k) {
-        const int t0 = w.r0 + k * ring.tile_rows;
-        ok = tc::warp_wait(&sh.empty[slot], freed.of(slot), &sh.abort, p.err, 1);
-        if (!ok) break;
-        freed.pass(slot);
-        copy_tile<kStreams>(p, &sh, smem, slot, t0, t0 + ring.tile_rows, true);
-        describe_tile(p, w, &sh, smem, slot, t0, t0 + ring.tile_rows, 0, &seen);
-        if (--slot < 0) slot = ring.slots - 1;
-      }
-    }
-    // the warps that compute wait for every copy, unless one of them gave up
-    if (!ok || *static_cast<volatile int*>(&sh.abort))
-      for (int k = 0; k < ring.slots; ++k)
-        if (sh.copies[k] > 0) tc::mbar_wait_drain(&sh.full[k], (sh.copies[k] - 1) & 1);
-    return;
   }
 
   if (threadIdx.x < 32) {
@@ -624,7 +587,7 @@ __global__ void __launch_bounds__(kBlock, 1) k_norm(const __grid_constant__ Args
   for (int k = 0; k < kStreams; ++k) step[k] = s.rp * ring.row_bytes[k];
   Op op(p, at);
   // structures without rows have zero statistics
-  if (!Op::kBackward && s.ptr)
+  if (!Op::kBackward && s.ptr && !copies)
     for (long long i = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x; i < s.n_structs;
          i += static_cast<long long>(gridDim.x) * kThreads)
       if (begin_of(s, static_cast<int>(i)) >= end_of(s, static_cast<int>(i)))
@@ -635,9 +598,10 @@ __global__ void __launch_bounds__(kBlock, 1) k_norm(const __grid_constant__ Args
   // ahead that it overwrites what the threads left. Where the ring is shorter than the block's rows, half
   // of it waits for that while the other half is read.
   const int half = ring.slots / 2, lost = w.tiles - ring.slots, room = ring.slots * ring.tile_rows;
-  int current = -1, n = at.row < s.rp ? w.r0 + at.row : INT_MAX, place = at.row;   // place: row n's for sums
+  int current = -1, n = at.row < s.rp ? w.r0 + at.row : INT_MAX;
+  int place = copies ? 0 : at.row;     // for sums: of the tile's first row, of row n
   int slot = 0, ended = 0, closed = 0, closed_at = 0, released = 0, released_slot = 0;
-  Phases full;
+  Phases phases;                       // of the full slots, of the empty ones where this warp copies
   Gate gate;
   auto forward = [&](const char* (&src)[kStreams], int rows_done) {
     n += rows_done * s.rp;
@@ -649,96 +613,135 @@ __global__ void __launch_bounds__(kBlock, 1) k_norm(const __grid_constant__ Args
     op.leave(acc + where * ring.acc_bytes, s.cv, at.col / V);
     op.clear();
   };
+  if (copies) {
+    Seen seen;
 #pragma unroll 1
-  for (int tile = 0; tile < w.tiles; ++tile) {
-    const int t0 = w.r0 + tile * ring.tile_rows, t1 = min(t0 + ring.tile_rows, w.r1);
-    if (!tc::warp_wait(&sh.full[slot], full.of(slot), &sh.abort, p.err, 2)) break;
-    full.pass(slot);
-    const int4 about = sh.tile[slot];
-    if (n < t1) {
-      const char* src[kStreams];
-      sources(slot, t0, n, src);
-      if (about.x != kMixed) {
-        if (about.x != current) {
-          current = about.x;
-          op.enter_up(p, at, current);
-        }
-        if constexpr (Op::kRows > 1) {
+    for (int k = 0; k < w.tiles; ++k) {
+      const int t0 = w.r0 + k * ring.tile_rows, t1 = min(t0 + ring.tile_rows, w.r1);
+      if (k >= held) {
+        if (!tc::warp_wait(&sh.empty[slot], phases.of(slot), &sh.abort, p.err, 1)) break;
+        phases.pass(slot);
+        copy_tile<kStreams>(p, &sh, smem, slot, t0, t1, k < last_once);
+      }
+      describe_tile(p, w, &sh, smem, slot, t0, t1, place, &seen);
+      if (++slot == ring.slots) slot = 0;
+      if ((place += ring.tile_rows) >= ring.acc_rows) place -= ring.acc_rows;
+    }
+  } else {
 #pragma unroll 1
-          while (n + (Op::kRows - 1) * s.rp < t1) {
-            op.template add<Op::kRows>(p, at, src, step, at.col);
-            forward(src, Op::kRows);
+    for (int tile = 0; tile < w.tiles; ++tile) {
+      const int t0 = w.r0 + tile * ring.tile_rows, t1 = min(t0 + ring.tile_rows, w.r1);
+      if (!tc::warp_wait(&sh.full[slot], phases.of(slot), &sh.abort, p.err, 2)) break;
+      phases.pass(slot);
+      const int4 about = sh.tile[slot];
+      if (n < t1) {
+        const char* src[kStreams];
+        sources(slot, t0, n, src);
+        if (about.x != kMixed) {
+          if (about.x != current) {
+            current = about.x;
+            op.enter_up(p, at, current);
           }
-        }
+          if constexpr (Op::kRows > 1) {
 #pragma unroll 1
-        while (n < t1) {
-          op.template add<1>(p, at, src, step, at.col);
-          forward(src, 1);
-        }
-        if (n >= about.y) leave(place >= s.rp ? place - s.rp : place - s.rp + ring.acc_rows);
-      } else {
-#pragma unroll 1
-        while (n < t1) {
-          const int2 e = rows[slot * ring.tile_rows + n - t0];
-          if (e.x >= 0) {
-            if (e.x != current) {
-              current = e.x;
-              op.enter_up(p, at, current);
+            while (n + (Op::kRows - 1) * s.rp < t1) {
+              op.template add<Op::kRows>(p, at, src, step, at.col);
+              forward(src, Op::kRows);
             }
-            op.template add<1>(p, at, src, step, at.col);
-            if (n + s.rp >= e.y) leave(place);
           }
-          forward(src, 1);
+#pragma unroll 1
+          while (n < t1) {
+            op.template add<1>(p, at, src, step, at.col);
+            forward(src, 1);
+          }
+          if (n >= about.y) leave(place >= s.rp ? place - s.rp : place - s.rp + ring.acc_rows);
+        } else {
+#pragma unroll 1
+          while (n < t1) {
+            const int2 e = rows[slot * ring.tile_rows + n - t0];
+            if (e.x >= 0) {
+              if (e.x != current) {
+                current = e.x;
+                op.enter_up(p, at, current);
+              }
+              op.template add<1>(p, at, src, step, at.col);
+              if (n + s.rp >= e.y) leave(place);
+            }
+            forward(src, 1);
+          }
         }
       }
+      ended = about.z;
+      if (released < lost && (ended == closed || tile - released + 1 >= half)) {
+        if (ended > closed) {
+          if (!gate.meet(&sh, p.err)) break;
+          close<Op>(p, acc, ends, closed_at, ended - closed);
+          closed_at += ended - closed;
+          if (closed_at >= room) closed_at -= room;
+          closed = ended;
+        }
+        __syncwarp();
+        for (; released <= tile && released < lost; ++released) {
+          tc::mbar_arrive_lane0(&sh.empty[released_slot], lane);
+          if (++released_slot == ring.slots) released_slot = 0;
+        }
+      }
+      if (++slot == ring.slots) slot = 0;
     }
-    ended = about.z;
-    if (released < lost && (ended == closed || tile - released + 1 >= half)) {
-      if (ended > closed) {
-        if (!gate.meet(&sh, p.err)) break;
-        close<Op>(p, acc, ends, closed_at, ended - closed);
-        closed_at += ended - closed;
-        if (closed_at >= room) closed_at -= room;
-        closed = ended;
-      }
-      __syncwarp();
-      for (; released <= tile && released < lost; ++released) {
-        tc::mbar_arrive_lane0(&sh.empty[released_slot], lane);
-        if (++released_slot == ring.slots) released_slot = 0;
-      }
-    }
-    if (++slot == ring.slots) slot = 0;
-  }
-  meet_compute();
-  if (!*static_cast<volatile int*>(&sh.abort) && ended > closed) close<Op>(p, acc, ends, closed_at, ended - closed);
-  if constexpr (Op::kBackward) {
-    // The block's channel sums, over the rows it reads side by side, in the room of the sums that are
-    // done with.
-    float* flat = reinterpret_cast<float*>(acc);
-    const int one = s.rp * s.channels;
-    float* chan = p.chan + static_cast<size_t>(blockIdx.x) * Q * s.channels;
+    meet_compute();
+    if (ended > closed) close<Op>(p, acc, ends, closed_at, ended - closed);
+    if constexpr (Op::kBackward) {
+      // The block's channel sums, over the rows it reads side by side, in the room of the sums that are
+      // done with.
+      float* flat = reinterpret_cast<float*>(acc);
+      const int one = s.rp * s.channels;
+      float* chan = p.chan + static_cast<size_t>(blockIdx.x) * Q * s.channels;
 #pragma unroll
-    for (int q = 0; q < Q; ++q) {
-      meet_compute();
-      if (at.row < s.rp) {
+      for (int q = 0; q < Q; ++q) {
+        meet_compute();
+        if (at.row < s.rp) {
 #pragma unroll
-        for (int k = 0; k < V; ++k) flat[at.row * s.channels + at.col + k] = op.own[q][k];
-      }
-      meet_compute();
+          for (int k = 0; k < V; ++k) flat[at.row * s.channels + at.col + k] = op.own[q][k];
+        }
+        meet_compute();
 #pragma unroll 1
-      for (int i = threadIdx.x; i < s.channels; i += kThreads) {
-        float t[4] = {};
+        for (int i = threadIdx.x; i < s.channels; i += kThreads) {
+          float t[4] = {};
 #pragma unroll 1
-        for (int r = i; r < one; r += 4 * s.channels)
+          for (int r = i; r < one; r += 4 * s.channels)
 #pragma unroll
-          for (int h = 0; h < 4; ++h) t[h] += r + h * s.channels < one ? flat[r + h * s.channels] : 0.0f;
-        chan[q * s.channels + i] = (t[0] + t[1]) + (t[2] + t[3]);
+            for (int h = 0; h < 4; ++h) t[h] += r + h * s.channels < one ? flat[r + h * s.channels] : 0.0f;
+          chan[q * s.channels + i] = (t[0] + t[1]) + (t[2] + t[3]);
+        }
       }
     }
   }
   __syncthreads();
+  const bool gave_up = *static_cast<volatile int*>(&sh.abort) != 0;   // by all threads before anyone goes on
   if (gridDim.x > 1) cg::this_grid().sync();
-  if (sh.abort) return;
+  else __syncthreads();
+
+  if (copies) {
+    if (p.out && !gave_up) {
+      // down again, from the slot of the last tile that the ring lost
+      Seen seen;
+      if (held == ring.slots && --slot < 0) slot = ring.slots - 1;
+#pragma unroll 1
+      for (int k = w.tiles - held - 1; k >= 0; --k) {
+        const int t0 = w.r0 + k * ring.tile_rows;
+        if (!tc::warp_wait(&sh.empty[slot], phases.of(slot), &sh.abort, p.err, 1)) break;
+        phases.pass(slot);
+        copy_tile<kStreams>(p, &sh, smem, slot, t0, t0 + ring.tile_rows, true);
+        describe_tile(p, w, &sh, smem, slot, t0, t0 + ring.tile_rows, 0, &seen);
+        if (--slot < 0) slot = ring.slots - 1;
+      }
+    }
+    // the block may not end before its copies have, also where a wait gave up
+    for (int k = 0; k < ring.slots; ++k)
+      if (sh.copies[k] > 0) tc::mbar_wait_drain(&sh.full[k], (sh.copies[k] - 1) & 1);
+    return;
+  }
+  if (gave_up) return;
 
   if constexpr (Op::kBackward) {
     // dw and db: a warp to a sum, its lanes to the blocks
@@ -773,8 +776,8 @@ __global__ void __launch_bounds__(kBlock, 1) k_norm(const __grid_constant__ Args
     const int t0 = w.r0 + tile * ring.tile_rows;
     if (--slot < 0) slot = min(ring.slots, w.tiles) - 1;
     if (tile < lost) {
-      if (!tc::warp_wait(&sh.full[slot], full.of(slot), &sh.abort, p.err, 2)) return;
-      full.pass(slot);
+      if (!tc::warp_wait(&sh.full[slot], phases.of(slot), &sh.abort, p.err, 2)) return;
+      phases.pass(slot);
     }
     if (n >= t0) {
       const int about = sh.tile[slot].x;

@@ -28,6 +28,20 @@ def test_plan_brings_every_byte_of_every_tile(tmp_path):
     assert run.returncode == 0 and run.stdout.strip().endswith(" 0 wrong"), run.stdout + run.stderr
 
 
+def test_all_threads_meet_at_the_same_barriers():
+    """A grid or block barrier has to be one statement for all threads of a block: none stands in a branch that
+    the copying warp or the computing ones take alone."""
+    with open(os.path.join(ROOT, "equivariant_mlip_tensor_edge_b200", "csrc", "etp_norm_sweep.h")) as f:
+        body = f.read().split("k_norm(const")[1].split("// ---------------------------------------------------------------- launch")[0]
+    assert body.count("this_grid().sync()") == 1
+    depth = 0
+    for line in body.splitlines():
+        if "__syncthreads()" in line:
+            assert depth == 1, line        # of the kernel's own block
+        depth += line.count("{") - line.count("}")
+    assert depth == 0
+
+
 def _check_forward(x, w, b, lmax, groups, ptr, act, out, stats, dtype):
     want, st = norm64(_np(x), w, b, lmax, groups, ptr, 1e-5, act)
     info = torch.finfo(TYPES[dtype])
