@@ -964,8 +964,9 @@ etp_status etp_group_norm_backward(int lmax, int channels, int groups, int n_nod
   const norm::Call c{lmax, channels, groups, n_nodes, n_structs, node_ptr, dtype, activation, zero_rest};
   etp_status st = check_norm(who, c, format, true, workspace, workspace_bytes);
   if (st != ETP_OK) return st;
-  if ((!grad_x && !grad_weight && !grad_bias) || (n_structs > 0 && !stats) ||
-      (n_nodes > 0 && (!grad_out || (format == ETP_CKPT_NONE ? !x : (!q || !scale))))) {
+  if ((n_structs > 0 && !stats) ||   // without rows an array of rows may be NULL, grad_x too
+      (n_nodes > 0 && ((!grad_x && !grad_weight && !grad_bias) || !grad_out ||
+                       (format == ETP_CKPT_NONE ? !x : (!q || !scale))))) {
     set_error(std::string(who) + ": NULL array, or no gradient asked for");
     return ETP_ERR_INVALID_ARG;
   }

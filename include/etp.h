@@ -335,7 +335,7 @@ etp_status etp_group_norm(int lmax, int channels, int groups, int n_nodes, int n
 
 /* Vector-Jacobian product of etp_group_norm for the cotangent grad_out (dtype): grad_x (dtype), and
  * grad_weight[lmax + 1][channels], grad_bias[channels] (float32, sums over all structures). Any may be
- * NULL, not all three. stats: from the forward. format ETP_CKPT_NONE: x is the forward's input;
+ * NULL, not all three (with n_nodes = 0, where grad_x has no values, also all). stats: from the forward. format ETP_CKPT_NONE: x is the forward's input;
  * otherwise x is ignored and the input is read from its checkpoint q, scale. Rows of no structure add
  * nothing; zero_rest as above, for grad_x. grad_x may not overlap grad_out or x.
  * x, grad_out, grad_x, q, scale: 16-byte aligned. */

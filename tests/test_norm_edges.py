@@ -1,5 +1,6 @@
 """Group norm and 8-bit checkpoints where sizes, ranges and arguments end: the launch plan replayed on the
 CPU, refusals, and kernels against float64 on the GPU."""
+import ctypes
 import os
 import shutil
 import subprocess
@@ -74,3 +75,31 @@ def test_short_rows_at_the_end_of_the_array(n, lmax, c, groups, dtype, keep):
     _check_forward(x, w, b, lmax, groups, ptr, "silu", out, stats, dtype)
     got = etp.group_norm_backward(ck if keep else xd, stats, wd, bd, g.to(DEV), lmax, groups, node_ptr)
     _check_backward(keep64(_np(x), keep)[0] if keep else _np(x), w, b, g, lmax, groups, ptr, "silu", stats, got, dtype)
+
+
+# ------------------------------------------------------------------ no rows
+
+def test_backward_without_rows_may_have_no_gradient_to_write():
+    """An empty grad_x has no address: asking for it alone is a valid call."""
+    lib, fake = etp.load_library(), ctypes.c_void_p(4096)
+
+    def bwd(n):
+        return lib.etp_group_norm_backward(1, 8, 2, n, 1, None, 0, None, 0, None, None, fake, None, None, 1, None, 0, None,
+                                           None, None, fake, 1 << 30, None)
+    assert bwd(0) == 0
+    assert bwd(1) == 1
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("keep", [None, "int8"])
+def test_gradients_of_no_rows(keep):
+    none = torch.empty(0, 32, device=DEV)
+    w, b = torch.ones(2, 8, device=DEV), torch.zeros(8, device=DEV)
+    ptr = torch.zeros(3, dtype=torch.int32, device=DEV)
+    out, stats, ck = etp.group_norm(none, w, b, 1, 2, ptr, checkpoint=keep)
+    gx, gw, gb = etp.group_norm_backward(ck if keep else none, stats, w, b, none, 1, 2, ptr, want_grad_affine=False)
+    assert gx.shape == (0, 32) and gw is None and gb is None
+    for affine in ((None, None), (w, b)):      # absent, and frozen
+        x = torch.empty(0, 32, device=DEV, requires_grad=True)
+        etp.group_norm_function(keep).apply(x, *affine, 1, 2, ptr).sum().backward()
+        assert x.grad.shape == (0, 32)
