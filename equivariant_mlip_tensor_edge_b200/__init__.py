@@ -431,6 +431,13 @@ def _named(table, name, what):
     return code
 
 
+def _fit_int(**sizes):
+    """Refuses sizes that a C int does not hold (ctypes would cut off their upper bits)."""
+    for what, v in sizes.items():
+        if not -1 << 31 <= v < 1 << 31:
+            raise ValueError(f"{what} must be below 2^31, got {v}")
+
+
 def _rows(t):
     """t contiguous and 16-byte aligned (a copy where it is not)."""
     t = t.contiguous()
@@ -504,6 +511,7 @@ class Checkpoint8:
         """The values the checkpoint stands for, in ``dtype`` (default: that of the activations)."""
         fmt, q, scale = self._checked()
         shape = q.shape
+        _fit_int(columns=shape[-1])
         if out is None:
             out = q.new_empty(shape, dtype=dtype or self.dtype)
         elif out.shape != shape or not out.is_contiguous() or (dtype is not None and out.dtype != dtype):
@@ -534,6 +542,7 @@ def checkpoint8(x, fmt="int8"):
     index = _one_device(x)
     if x.dim() < 1:
         raise ValueError("x needs at least one dimension")
+    _fit_int(columns=x.shape[-1])
     dtype = _dtype_code(x.dtype)
     x = x.contiguous()
     ck = _empty_checkpoint(x, code)
@@ -563,7 +572,9 @@ def _norm_shape(shape, lmax, groups, node_ptr, weight, bias):
         raise ValueError(f"weight must be [{lmax + 1}, {c}], got {tuple(weight.shape)}")
     if bias is not None and bias.shape != (c,):
         raise ValueError(f"bias must be [{c}], got {tuple(bias.shape)}")
-    return n, c, 1 if node_ptr is None else node_ptr.numel() - 1
+    s = 1 if node_ptr is None else node_ptr.numel() - 1
+    _fit_int(rows=n, channels=c, groups=groups, structures=s)
+    return n, c, s
 
 
 def _norm_workspace(lmax, c, groups, s, backward, x, workspace):

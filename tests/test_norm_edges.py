@@ -103,3 +103,27 @@ def test_gradients_of_no_rows(keep):
         x = torch.empty(0, 32, device=DEV, requires_grad=True)
         etp.group_norm_function(keep).apply(x, *affine, 1, 2, ptr).sum().backward()
         assert x.grad.shape == (0, 32)
+
+
+# ------------------------------------------------------------------ sizes past a C int
+
+@pytest.mark.parametrize("cols", [1 << 32, (1 << 32) + 64, 1 << 31])
+def test_binding_refuses_sizes_past_a_c_int(monkeypatch, cols):
+    """Sizes of 2^31 and more are refused, not cut to their lower 32 bits (tensors without memory here)."""
+    monkeypatch.setattr(etp, "_one_device", lambda *tensors: 0)
+    monkeypatch.setattr(etp, "_call", lambda index, where, *args: pytest.fail(f"{where} was called"))
+    meta = dict(device="meta")
+    x = torch.empty(cols, dtype=torch.bfloat16, **meta)
+    ck = etp.Checkpoint8(torch.empty(cols, dtype=torch.int8, **meta), torch.empty(-(-cols // 32), dtype=torch.uint8, **meta),
+                         torch.bfloat16)
+    tall, wide = x.view(cols, 1), x.view(1, cols)
+    many = torch.empty(cols + 1, dtype=torch.int32, **meta)
+    few = torch.empty(4, 1, dtype=torch.bfloat16, **meta)
+    stats = torch.empty(1, 2, 1, **meta)
+    for call in (lambda: etp.checkpoint8(x), lambda: etp.checkpoint8(wide), ck.restore,
+                 lambda: etp.group_norm(tall, None, None, 0, 1), lambda: etp.group_norm(wide, None, None, 0, 1),
+                 lambda: etp.group_norm(few, None, None, 0, cols + 1), lambda: etp.group_norm(few, None, None, 0, 1, many),
+                 lambda: etp.group_norm_backward(tall, stats, None, None, tall, 0, 1),
+                 lambda: etp.group_norm_backward(wide, stats, None, None, wide, 0, 1)):
+        with pytest.raises(ValueError, match="2\\^31"):
+            call()
