@@ -111,7 +111,7 @@ void launch_vectors(bool int8, long long rows, int cols, int blocks, T* x, uint8
   p.blocks = blocks;
   p.d_block = static_cast<int>(p.stride % blocks);
   p.d_off = p.stride / blocks * cols + static_cast<long long>(p.d_block) * kCkptBlock;
-  p.wrap = cols - blocks * kCkptBlock;
+  p.wrap = static_cast<int>(cols - static_cast<long long>(blocks) * kCkptBlock);
   if (cols % kCkptBlock == 0) k_vectors<T, kStore, true><<<grid, kThreads, 0, s>>>(p, int8, x, q, scale);
   else k_vectors<T, kStore, false><<<grid, kThreads, 0, s>>>(p, int8, x, q, scale);
 }
@@ -256,7 +256,7 @@ void launch_units(bool int8, long long rows, int cols, int blocks, T* x, uint8_t
   p.rows = rows;
   p.cols = cols;
   p.blocks = blocks;
-  p.per_row = (cols + kUnit - 1) / kUnit;
+  p.per_row = (cols - 1) / kUnit + 1;
   p.seg = p.per_row > 1 ? kUnit : cols;
   p.unit_rows = p.per_row > 1 ? 1 : kUnit / cols;
   p.n = (rows + p.unit_rows - 1) / p.unit_rows * p.per_row;
@@ -272,7 +272,7 @@ bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % 
 template <class T, bool kStore>
 etp_status run(bool int8, long long rows, int cols, void* x, uint8_t* q, uint8_t* scale, cudaStream_t s) {
   T* xt = static_cast<T*>(x);
-  const int blocks = (cols + kCkptBlock - 1) / kCkptBlock;
+  const int blocks = (cols - 1) / kCkptBlock + 1;   // cols > 0; cols + 31 may not fit an int
   if (cols % 4 == 0 && aligned(x, 4 * sizeof(T)) && aligned(q, 4))
     launch_vectors<T, kStore>(int8, rows, cols, blocks, xt, q, scale, s);
   else

@@ -127,3 +127,21 @@ def test_binding_refuses_sizes_past_a_c_int(monkeypatch, cols):
                  lambda: etp.group_norm_backward(wide, stats, None, None, wide, 0, 1)):
         with pytest.raises(ValueError, match="2\\^31"):
             call()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("cols", [(1 << 31) - 1, (1 << 31) - 4])
+def test_checkpoint_of_the_longest_rows(cols):
+    """One row of nearly 2^31 values has the codes of the same values in rows of 32 (whose tail is checked apart)."""
+    if torch.cuda.mem_get_info()[0] < 24 << 30:
+        pytest.skip("needs 24 GB")
+    x = torch.empty(cols, dtype=torch.bfloat16, device=DEV).normal_()
+    ck = etp.checkpoint8(x)
+    whole = cols // 32 * 32
+    rows = etp.checkpoint8(x[:whole].view(-1, 32))
+    assert torch.equal(ck.q[:whole].view(-1, 32), rows.q) and torch.equal(ck.scale[:-1], rows.scale[:, 0])
+    held, codes, byte = keep64(_np(x[whole:])[None], "int8")
+    assert (_np(ck.q[whole:]) == codes).all() and int(ck.scale[-1]) == byte[0, 0]
+    back = ck.restore()
+    assert torch.equal(back[:whole].view(-1, 32), rows.restore())
+    assert (_np(back[whole:]) == _np(torch.from_numpy(held).to(torch.bfloat16))).all()
