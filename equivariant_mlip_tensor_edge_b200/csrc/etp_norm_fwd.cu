@@ -80,13 +80,19 @@ struct Fwd {
     return l == 0 ? d[cv + i] : reinterpret_cast<const float*>(d + 2 * cv)[(l - 1) * cv + i];
   }
 
-  // Statistics of rank l of n rows of a group, from sum x (l = 0) and sum x^2: r_l, and mu for l = 0.
+  // Statistics of rank l of n rows of a group, from sum x (l = 0) and sum x^2: r_l, and mu for l = 0. The
+  // variance of l = 0 is (N sum x^2 - (sum x)^2) / N^2, with the rounding errors of both products added
+  // back: what cancels is as good as the sums are.
   static __device__ float2 value(const Args& p, int l, int n, double s0, double s1) {
-    const double inv = reciprocal(static_cast<double>(n) * p.s.cg * (2 * l + 1));
-    const double m = l == 0 ? s0 * inv : 0.0;
-    double var = fma(-m, m, s1 * inv);
+    const double count = static_cast<double>(n) * p.s.cg * (2 * l + 1), inv = reciprocal(count);
+    double var = s1 * inv;
+    if (l == 0) {
+      const double a = count * s1, b = s0 * s0;
+      var = ((a - b) + (fma(count, s1, -a) - fma(s0, s0, -b))) * inv * inv;
+    }
     if (var < 0.0) var = 0.0;   // not fmax, which would drop a NaN
-    return make_float2(static_cast<float>(m), rsqrtf(static_cast<float>(var + static_cast<double>(p.eps))));
+    return make_float2(l == 0 ? static_cast<float>(s0 * inv) : 0.0f,
+                       rsqrtf(static_cast<float>(var + static_cast<double>(p.eps))));
   }
 
   __device__ __forceinline__ void enter_down(const Args& p, const Place& at, int, const float* st) {

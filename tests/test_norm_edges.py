@@ -5,6 +5,7 @@ import os
 import shutil
 import subprocess
 
+import numpy as np
 import pytest
 
 from tests._norm_side import keep64, norm64, norm_bounds
@@ -145,3 +146,24 @@ def test_checkpoint_of_the_longest_rows(cols):
     back = ck.restore()
     assert torch.equal(back[:whole].view(-1, 32), rows.restore())
     assert (_np(back[whole:]) == _np(torch.from_numpy(held).to(torch.bfloat16))).all()
+
+
+# ------------------------------------------------------------------ precision
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("offset,step", [(1e4, 2.0 ** -8), (1e5, 2.0 ** -6), (1e6, 2.0 ** -4)])
+def test_deviation_of_values_far_from_zero(offset, step):
+    """Scalars of spread 1 far from zero, in multiples of `step` of under 2^24 steps, at most 32 to a sum: the
+    sums of x and x^2 are exact in 64 bits, so nothing but what is made of them can spoil the deviation."""
+    rng = np.random.default_rng(11)
+    n, c, groups = 200, 32, 8
+    x = np.round((offset + rng.standard_normal((n, 4 * c))) / step) * step
+    x[:, c:] -= offset
+    assert np.abs(x).max() / step < 1 << 24 and (x.astype(np.float32) == x).all()
+    ptr = [0, 1] + list(range(8, n, 8)) + [n]     # structures of up to 8 rows, of 4 channels a group
+    out, stats, _ = etp.group_norm(torch.from_numpy(x).float().to(DEV), None, None, 1, groups,
+                                   torch.tensor(ptr, dtype=torch.int32, device=DEV))
+    want, st = norm64(x, None, None, 1, groups, ptr, 1e-5, "silu")
+    _within(_np(stats)[:, 0], st[:, 0], 2.0 ** -24 * np.abs(st[:, 0]), "mean")
+    _within(_np(stats)[:, 1:], st[:, 1:], 16 * 2.0 ** -24 * st[:, 1:], "deviation")
+    _within(_np(out), want, norm_bounds(x, None, None, 1, groups, ptr, "silu", st, 0), "out")
