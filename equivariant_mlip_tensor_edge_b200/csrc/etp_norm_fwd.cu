@@ -15,10 +15,9 @@ struct Fwd {
   static constexpr int kRows = K == 1 ? 4 : K == 4 ? 2 : 1;   // rows at once: more loads under way where a row has few
   static constexpr int kLanes = kCkptBlock / V;   // threads that share a checkpoint block
 
-  static constexpr int kAcc = 16 + 4 * L;         // bytes of a thread's sums: two of 64 bits, L of 32
+  static constexpr int kAcc = 8 * Q;              // bytes of a thread's sums
 
-  double t[2];
-  float u[L + 1];
+  double t[Q];                                    // sum x (l = 0) and sum x^2 of every rank
   float w[L + 1][V], bias[V], wr[L + 1][V], mu;   // wr: w_l r_l of the structure at hand
 
   __device__ Fwd(const Args& p, const Place& at) {
@@ -28,13 +27,13 @@ struct Fwd {
     clear();
   }
   __device__ void clear() {
-    t[0] = t[1] = 0.0;
 #pragma unroll
-    for (int l = 0; l <= L; ++l) u[l] = 0.0f;
+    for (int q = 0; q < Q; ++q) t[q] = 0.0;
   }
   __device__ void enter_up(const Args&, const Place&, int) {}
 
-  // t += x, x^2 (l = 0); u_l += x^2 (no cancellation: in 32 bits); rows `step` bytes apart
+  // Of l > 0 a row's squares (at most 28 to a thread, no cancellation) are added in 32 bits; the rest in 64.
+  // Rows `step` bytes apart.
   template <int R>
   __device__ void add(const Args& p, const Place&, const char* const (&src)[kStreams], const int (&step)[kStreams], int) {
     float v[R][K][V];
@@ -61,23 +60,18 @@ struct Fwd {
         for (int m = l * l; m < (l + 1) * (l + 1); ++m)
 #pragma unroll
           for (int k = 0; k < V; ++k) row = fmaf(v[h][m][k], v[h][m][k], row);
-        u[l] += row;
+        t[1 + l] += row;
       }
     }
   }
-  // a row's place for sums: [2][cv] of 64 bits, [L][cv] of 32
+  // a row's place for sums: [Q][cv]
   __device__ void leave(char* acc, int cv, int i) {
-    double* d = reinterpret_cast<double*>(acc);
-    d[i] = t[0];
-    d[cv + i] = t[1];
-    float* f = reinterpret_cast<float*>(d + 2 * cv);
 #pragma unroll
-    for (int l = 1; l <= L; ++l) f[(l - 1) * cv + i] = u[l];
+    for (int q = 0; q < Q; ++q) reinterpret_cast<double*>(acc)[q * cv + i] = t[q];
   }
   static __device__ __forceinline__ double first(const char* acc, int, int i) { return reinterpret_cast<const double*>(acc)[i]; }
   static __device__ __forceinline__ double second(const char* acc, int cv, int l, int i) {
-    const double* d = reinterpret_cast<const double*>(acc);
-    return l == 0 ? d[cv + i] : reinterpret_cast<const float*>(d + 2 * cv)[(l - 1) * cv + i];
+    return reinterpret_cast<const double*>(acc)[(1 + l) * cv + i];
   }
 
   // Statistics of rank l of n rows of a group, from sum x (l = 0) and sum x^2: r_l, and mu for l = 0. The

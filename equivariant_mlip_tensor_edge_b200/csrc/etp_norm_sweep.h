@@ -19,10 +19,11 @@
 // first sweep goes up, the second comes down, so what the ring holds at the turn (all of it, where the
 // rows fit on the chip) is not read again, and what comes next was read last and is likely in L2. A
 // structure that crosses blocks (two at most for a block: one that reaches in from before, one that goes
-// on behind) leaves partial sums, which meet after the grid barrier between the sweeps. Sums are kept in
-// 64 bits where they cancel (x and x^2 of l = 0: a mean far larger than the spread) and from thread to
-// thread; a thread adds its own rows of the others in 32. Every sum has one order, so equal calls give
-// equal bits.
+// on behind) leaves partial sums, which meet after the grid barrier between the sweeps. The forward keeps
+// its sums in 64 bits, but for a row's squares of l > 0. The backward adds in 32 bits within a block, a
+// thread's rows and then the threads (joining the threads in 64 bits took the backward of 4000 structures
+// from 24.4 to 25.9 us), and in 64 from block to block. Every sum has one order, so equal calls give equal
+// bits.
 //
 // A thread holds V neighbouring channels (V = 4, 2 or 1, as the group size divides by it) of every rp-th
 // row and walks the row's components, so a channel's gate stays in its thread. Sums stay in

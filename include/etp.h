@@ -323,8 +323,9 @@ size_t etp_group_norm_workspace_bytes(int lmax, int channels, int groups, int n_
  * they were in out, or zeroed if zero_rest is nonzero. format: ETP_CKPT_NONE, or the checkpoint of all
  * rows of x is stored to q and scale as by etp_checkpoint_store (q 16-byte aligned), in the same
  * pass when channels % 32 == 0. lmax 0..3; channels / groups whole, groups <= 64, dim <= 4096, channels
- * <= 1024, 512 or 256 as channels / groups is a multiple of 4, of 2 or odd; eps >= 0. Sums are taken
- * in 64 bits where they cancel or join threads, else in 32; equal calls give equal bits. Asynchronous
+ * <= 1024, 512 or 256 as channels / groups is a multiple of 4, of 2 or odd; eps >= 0. The
+ * statistics' sums are taken in 64 bits (a row's squares of l > 0 in 32), the backward's in 32 within
+ * a thread block and 64 between blocks; equal calls give equal bits. Asynchronous
  * (a cooperative launch); concurrent calls need a workspace each, 256-byte aligned. With ETP_VALIDATE=1
  * node_ptr is checked first (ETP_ERR_BAD_GRAPH), and the call waits and returns ETP_ERR_CUDA if a
  * bounded pipeline wait gave up. */

@@ -167,3 +167,21 @@ def test_deviation_of_values_far_from_zero(offset, step):
     _within(_np(stats)[:, 0], st[:, 0], 2.0 ** -24 * np.abs(st[:, 0]), "mean")
     _within(_np(stats)[:, 1:], st[:, 1:], 16 * 2.0 ** -24 * st[:, 1:], "deviation")
     _within(_np(out), want, norm_bounds(x, None, None, 1, groups, ptr, "silu", st, 0), "out")
+
+
+@pytest.mark.gpu
+def test_deviation_of_a_long_structure():
+    """100048 equal rows of 1024 channels: 676 to a thread, whose squares of l > 0 a 32-bit sum would round
+    the same way each time (56 x 2^-24 in the end). Within the bound of the short ones: a row's squares in
+    32 bits, the rest in 64."""
+    if torch.cuda.mem_get_info()[0] < 8 << 30:
+        pytest.skip("needs 8 GB")
+    n, c, groups = 148 * 676, 1024, 64
+    row = torch.full((1, 4 * c), 0.9, device=DEV)
+    row[:, :c:2] = -0.9
+    out, stats, _ = etp.group_norm(row.expand(n, -1), None, None, 1, groups)
+    want, st = norm64(_np(row), None, None, 1, groups, [0, 1], 1e-5, "silu")
+    _within(_np(stats)[:, 1:], st[:, 1:], 16 * 2.0 ** -24 * st[:, 1:], "deviation")
+    bound = norm_bounds(_np(row), None, None, 1, groups, [0, 1], "silu", st, 0)
+    for r in (0, n // 2, n - 1):
+        _within(_np(out[r:r + 1]), want, bound, "out")
