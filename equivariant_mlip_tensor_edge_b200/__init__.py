@@ -60,6 +60,8 @@ SIGNATURES = {
     "etp_group_norm": (_i, [_i, _i, _i, _i, _i, _vp, _i, _vp, _vp, _vp, _f, _i, _i, _vp, _vp, _i, _vp, _vp, _vp, _sz, _vp]),
     "etp_group_norm_backward": (_i, [_i, _i, _i, _i, _i, _vp, _i, _vp, _i, _vp, _vp, _vp, _vp, _vp, _i, _vp, _i, _vp, _vp,
                                      _vp, _vp, _sz, _vp]),
+    "etp_group_norm_status": (_i, [_vp, _ip]),
+    "etp_group_norm_status_word": (_ip, []),
     "etp_forces": (_i, [_i, _i, _vp, _vp, _vp, _vp, _vp, _vp]),
     "etp_graph_workspace_bytes": (_sz, [_i, _i]),
     "etp_neighbors": (_i, [_vp, _i, _dp, _ip, _f, _i, _ip, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
@@ -664,6 +666,14 @@ def group_norm_backward(x, stats, weight, bias, grad_out, lmax, groups, node_ptr
           _addr(scale), stats.data_ptr(), _addr(weight), _addr(bias), act, grad_out.data_ptr(), made,
           grad_x.data_ptr() if want_grad_x else None, _addr(gw), _addr(gb), ws.data_ptr(), nb)
     return (grad_x if want_grad_x else None), gw, gb
+
+
+def group_norm_check_status(device=None):
+    """Synchronise the current stream and raise if a kernel of an earlier group_norm or group_norm_backward
+    call gave up a bounded pipeline wait (the code is cleared). Until then later calls raise."""
+    code = ctypes.c_int(0)
+    stream = _stream(device) if device is not None else None
+    _check(load_library().etp_group_norm_status(stream, ctypes.byref(code)), "etp_group_norm_status")
 
 
 def group_norm_function(checkpoint=None):

@@ -4,6 +4,7 @@
 #include <climits>
 #include <cstdlib>
 #include <cstring>
+#include <mutex>
 #include <new>
 #include <string>
 #include <vector>
@@ -18,10 +19,16 @@ struct etp_ctx {
 
 namespace {
 
-// Gives the handle its sticky status word: pinned host memory mapped into the device address space
-// where a device is present (the kernels store their timeout codes there), plain host memory
-// otherwise (no kernel can run then). Returns false on failure (message set).
-bool attach_status_word(etp_ctx* h) {
+// A sticky status word: pinned host memory mapped into the device address space where a device is
+// present (the kernels store their timeout codes there), plain host memory otherwise (no kernel can
+// run then). host is NULL until it is made.
+struct StatusWord {
+  int *host = nullptr, *dev = nullptr;
+  bool mapped = false;
+};
+
+// Returns false on failure (message set).
+bool make_status_word(StatusWord* w, const char* who) {
   int ndev = 0;
   cudaError_t e = cudaGetDeviceCount(&ndev);
   if (e == cudaSuccess && ndev > 0) {
@@ -31,25 +38,48 @@ bool attach_status_word(etp_ctx* h) {
     if (e == cudaSuccess) e = cudaHostGetDevicePointer(&d, p, 0);
     if (e != cudaSuccess) {
       if (p) cudaFreeHost(p);
-      etp::cuda_status(e, "etp_create: pinned status word");
+      etp::cuda_status(e, (std::string(who) + ": pinned status word").c_str());
       return false;
     }
     *static_cast<volatile int*>(p) = 0;
-    h->c.status = static_cast<int*>(p);
-    h->c.status_dev = static_cast<int*>(d);
-    h->c.status_mapped = true;
+    w->host = static_cast<int*>(p);
+    w->dev = static_cast<int*>(d);
+    w->mapped = true;
     return true;
   }
   cudaGetLastError();   // no device: clear the runtime's error state
   void* p = std::calloc(1, 64);
   if (!p) {
-    etp::set_error("etp_create: out of host memory");
+    etp::set_error(std::string(who) + ": out of host memory");
     return false;
   }
-  h->c.status = static_cast<int*>(p);
-  h->c.status_dev = nullptr;
-  h->c.status_mapped = false;
+  w->host = static_cast<int*>(p);
   return true;
+}
+
+bool attach_status_word(etp_ctx* h) {
+  StatusWord w;
+  if (!make_status_word(&w, "etp_create")) return false;
+  h->c.status = w.host;
+  h->c.status_dev = w.dev;
+  h->c.status_mapped = w.mapped;
+  return true;
+}
+
+// The word of the group norm, whose calls have no handle: one of the process, made by the first call that
+// needs it (also while a stream is being captured) and kept to the end.
+const StatusWord* norm_status() {
+  static std::mutex lock;
+  static StatusWord word;
+  std::lock_guard<std::mutex> hold(lock);
+  if (!word.host) {
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    const bool swapped = cudaThreadExchangeStreamCaptureMode(&mode) == cudaSuccess;
+    make_status_word(&word, "etp_group_norm");
+    if (swapped) cudaThreadExchangeStreamCaptureMode(&mode);
+    else cudaGetLastError();
+  }
+  return word.host ? &word : nullptr;
 }
 
 void release_status_word(etp_ctx* h) {
@@ -416,25 +446,29 @@ etp_status etp_destroy(etp_handle h) {
 
 int* etp_status_word(etp_handle h) { return h ? h->c.status : nullptr; }
 
+static etp_status read_status(int* word, bool mapped, void* stream, int* code, const char* who) {
+  if (mapped) {
+    cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_status(e, (std::string(who) + ": stream synchronisation").c_str());
+  }
+  volatile int* w = word;
+  const int v = w ? *w : 0;
+  if (w) *w = 0;
+  if (code) *code = v;
+  if (v != 0) {
+    set_error(std::string(who) + ": a bounded pipeline wait gave up (code " + std::to_string(v) +
+              "); outputs of the calls since the previous check may be incomplete");
+    return ETP_ERR_CUDA;
+  }
+  return ETP_OK;
+}
+
 etp_status etp_get_status(etp_handle h, void* stream, int* code) {
   if (!h) {
     set_error("etp_get_status: NULL handle");
     return ETP_ERR_INVALID_ARG;
   }
-  if (h->c.status_mapped) {
-    cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
-    if (e != cudaSuccess) return cuda_status(e, "etp_get_status: stream synchronisation");
-  }
-  volatile int* w = reinterpret_cast<volatile int*>(h->c.status);
-  const int v = w ? *w : 0;
-  if (w) *w = 0;
-  if (code) *code = v;
-  if (v != 0) {
-    set_error("etp_get_status: a bounded pipeline wait gave up (code " + std::to_string(v) +
-              "); outputs of the calls since the previous check may be incomplete");
-    return ETP_ERR_CUDA;
-  }
-  return ETP_OK;
+  return read_status(h->c.status, h->c.status_mapped, stream, code, "etp_get_status");
 }
 
 etp_status etp_get_info(etp_handle h, etp_info_t* info) {
@@ -923,6 +957,37 @@ static etp_status check_norm(const char* who, const norm::Call& c, etp_ckpt_form
   return ETP_OK;
 }
 
+int* etp_group_norm_status_word(void) {
+  const StatusWord* w = norm_status();
+  return w ? w->host : nullptr;
+}
+
+etp_status etp_group_norm_status(void* stream, int* code) {
+  const StatusWord* w = norm_status();
+  if (!w) return ETP_ERR_CUDA;
+  return read_status(w->host, w->mapped, stream, code, "etp_group_norm_status");
+}
+
+// Refuses a call after a kernel of an earlier one gave up a wait; otherwise *word is the status word.
+static etp_status norm_gate(const char* who, const StatusWord** word) {
+  *word = norm_status();
+  if (!*word) return ETP_ERR_CUDA;
+  const int code = *static_cast<volatile int*>((*word)->host);
+  if (code == 0) return ETP_OK;
+  set_error(std::string(who) + ": a kernel of an earlier group norm call gave up a bounded wait (code " + std::to_string(code) +
+            "); outputs since then may be incomplete; etp_group_norm_status reads and clears it");
+  return ETP_ERR_CUDA;
+}
+
+// With ETP_VALIDATE=1 a call waits for its kernel and reports its code.
+static etp_status norm_finished(const char* who, cudaStream_t s) {
+  if (!validate_requested()) return ETP_OK;
+  cudaError_t e = cudaStreamSynchronize(s);
+  if (e != cudaSuccess) return cuda_status(e, who);
+  const StatusWord* word = nullptr;
+  return norm_gate(who, &word);
+}
+
 etp_status etp_group_norm(int lmax, int channels, int groups, int n_nodes, int n_structs, const int* node_ptr,
                           etp_dtype dtype, const void* x, const float* weight, const float* bias, float eps,
                           etp_activation activation, int zero_rest, void* out, float* stats, etp_ckpt_format format,
@@ -944,14 +1009,16 @@ etp_status etp_group_norm(int lmax, int channels, int groups, int n_nodes, int n
     set_error(std::string(who) + ": out may not overlap x");
     return ETP_ERR_INVALID_ARG;
   }
+  const StatusWord* word = nullptr;
+  if ((st = norm_gate(who, &word)) != ETP_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (n_nodes == 0)
     return n_structs == 0 ? ETP_OK
                           : cuda_status(cudaMemsetAsync(stats, 0, sizeof(float) * n_structs * (lmax + 2) * groups, s), who);
   if (validate_requested() && (st = norm::validate(c, workspace, s)) != ETP_OK) return st;
   st = norm::forward(c, x, weight, bias, eps, out, stats, format, static_cast<uint8_t*>(q),
-                     static_cast<uint8_t*>(scale), workspace, s);
-  return st == ETP_OK && validate_requested() ? norm::finished(workspace, s, who) : st;
+                     static_cast<uint8_t*>(scale), workspace, word->dev, s);
+  return st == ETP_OK ? norm_finished(who, s) : st;
 }
 
 etp_status etp_group_norm_backward(int lmax, int channels, int groups, int n_nodes, int n_structs,
@@ -979,6 +1046,8 @@ etp_status etp_group_norm_backward(int lmax, int channels, int groups, int n_nod
     set_error(std::string(who) + ": grad_x may not overlap grad_out or x");
     return ETP_ERR_INVALID_ARG;
   }
+  const StatusWord* word = nullptr;
+  if ((st = norm_gate(who, &word)) != ETP_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (n_nodes == 0) {
     cudaError_t e = grad_weight ? cudaMemsetAsync(grad_weight, 0, sizeof(float) * (lmax + 1) * channels, s) : cudaSuccess;
@@ -987,8 +1056,8 @@ etp_status etp_group_norm_backward(int lmax, int channels, int groups, int n_nod
   }
   if (validate_requested() && (st = norm::validate(c, workspace, s)) != ETP_OK) return st;
   st = norm::backward(c, x, format, static_cast<const uint8_t*>(q), static_cast<const uint8_t*>(scale), stats, weight,
-                      bias, grad_out, grad_x, grad_weight, grad_bias, workspace, s);
-  return st == ETP_OK && validate_requested() ? norm::finished(workspace, s, who) : st;
+                      bias, grad_out, grad_x, grad_weight, grad_bias, workspace, word->dev, s);
+  return st == ETP_OK ? norm_finished(who, s) : st;
 }
 
 etp_status etp_radial_weights(etp_handle h, int n_edges, const float* edge_vec, const float* W,

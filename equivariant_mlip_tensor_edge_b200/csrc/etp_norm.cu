@@ -15,7 +15,7 @@ int vector_width(int channels, int groups) {
   return cg % 4 == 0 ? 4 : cg % 2 == 0 ? 2 : 1;
 }
 
-// workspace: [error word][partial sums][means per structure][channel sums per block], the last two
+// workspace: [flag of the check of node_ptr][partial sums][means per structure][channel sums per block], the last two
 // for the backward
 size_t partial_bytes(const Call& c) {
   return align256(static_cast<size_t>(kMaxBlocks) * 2 * (c.lmax + 2) * c.groups * sizeof(double));
@@ -31,13 +31,6 @@ __global__ void k_check_ptr(const int* ptr, int n_structs, int n_nodes, int* fla
   if (v < 0 || v > n_nodes || (i < n_structs && ptr[i + 1] < v)) *flag = 1;
 }
 
-// Waits for the stream and reads the int at the start of the workspace.
-etp_status read_flag(void* ws, int* value, cudaStream_t s, const char* what) {
-  cudaError_t e = cudaMemcpyAsync(value, ws, sizeof(int), cudaMemcpyDeviceToHost, s);
-  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-  return e == cudaSuccess ? ETP_OK : cuda_status(e, what);
-}
-
 }  // namespace
 
 etp_status validate(const Call& c, void* ws, cudaStream_t s) {
@@ -49,18 +42,12 @@ etp_status validate(const Call& c, void* ws, cudaStream_t s) {
   }
   if (e != cudaSuccess) return cuda_status(e, "node_ptr validation");
   int bad = 0;
-  etp_status st = read_flag(ws, &bad, s, "node_ptr validation");
-  if (st != ETP_OK || !bad) return st;
+  e = cudaMemcpyAsync(&bad, ws, sizeof(int), cudaMemcpyDeviceToHost, s);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  if (e != cudaSuccess) return cuda_status(e, "node_ptr validation");
+  if (!bad) return ETP_OK;
   set_error("node_ptr must be ascending and stay within [0, n_nodes]");
   return ETP_ERR_BAD_GRAPH;
-}
-
-etp_status finished(void* ws, cudaStream_t s, const char* who) {
-  int code = 0;
-  etp_status st = read_flag(ws, &code, s, who);
-  if (st != ETP_OK || !code) return st;
-  set_error(std::string(who) + ": a bounded pipeline wait gave up (code " + std::to_string(code) + "); the output is incomplete");
-  return ETP_ERR_CUDA;
 }
 
 bool supported(int lmax, int channels, int groups) {
@@ -75,7 +62,8 @@ size_t workspace_bytes(const Call& c, bool backward) {
 }
 
 etp_status forward(const Call& c, const void* x, const float* weight, const float* bias, float eps, void* out,
-                   float* stats, etp_ckpt_format format, uint8_t* q, uint8_t* scale, void* ws, cudaStream_t s) {
+                   float* stats, etp_ckpt_format format, uint8_t* q, uint8_t* scale, void* ws, int* err,
+                   cudaStream_t s) {
   Args p{};
   p.ring.src[0] = static_cast<const char*>(x);
   p.weight = weight;
@@ -86,7 +74,7 @@ etp_status forward(const Call& c, const void* x, const float* weight, const floa
   p.out = out;
   p.table = stats;
   p.int8 = format == ETP_CKPT_INT8;
-  p.err = static_cast<int*>(ws);
+  p.err = err;
   p.part = reinterpret_cast<double*>(static_cast<char*>(ws) + 256);
   // the norm writes the checkpoint itself where no block of 32 crosses a component's end
   const bool fused = format != ETP_CKPT_NONE && c.channels % kCkptBlock == 0;
@@ -103,7 +91,7 @@ etp_status forward(const Call& c, const void* x, const float* weight, const floa
 
 etp_status backward(const Call& c, const void* x, etp_ckpt_format format, const uint8_t* q, const uint8_t* scale,
                     const float* stats, const float* weight, const float* bias, const void* grad_out, void* grad_x,
-                    float* grad_weight, float* grad_bias, void* ws, cudaStream_t s) {
+                    float* grad_weight, float* grad_bias, void* ws, int* err, cudaStream_t s) {
   const bool kept = format != ETP_CKPT_NONE;
   Args p{};
   p.ring.src[0] = static_cast<const char*>(grad_out);
@@ -118,7 +106,7 @@ etp_status backward(const Call& c, const void* x, etp_ckpt_format format, const 
   p.out = grad_x;
   p.grad_weight = grad_weight;
   p.grad_bias = grad_bias;
-  p.err = static_cast<int*>(ws);
+  p.err = err;
   char* at = static_cast<char*>(ws) + 256;
   p.part = reinterpret_cast<double*>(at);
   p.table = reinterpret_cast<float*>(at += partial_bytes(c));

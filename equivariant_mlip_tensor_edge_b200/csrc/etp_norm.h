@@ -17,17 +17,16 @@ struct Call {
   int activation, zero_rest;
 };
 
-// ETP_ERR_CUDA if a bounded wait of the call that used ws gave up (synchronises s).
-etp_status finished(void* ws, cudaStream_t s, const char* who);
 bool supported(int lmax, int channels, int groups);
 // ETP_ERR_BAD_GRAPH unless node_ptr ascends within [0, n_nodes] (synchronises s).
 etp_status validate(const Call& c, void* ws, cudaStream_t s);
 size_t workspace_bytes(const Call& c, bool backward);
+// err: a word on the device or mapped for it that receives the code of a bounded wait that gave up.
 etp_status forward(const Call& c, const void* x, const float* weight, const float* bias, float eps, void* out,
-                   float* stats, etp_ckpt_format format, uint8_t* q, uint8_t* scale, void* ws, cudaStream_t s);
+                   float* stats, etp_ckpt_format format, uint8_t* q, uint8_t* scale, void* ws, int* err, cudaStream_t s);
 etp_status backward(const Call& c, const void* x, etp_ckpt_format format, const uint8_t* q, const uint8_t* scale,
                     const float* stats, const float* weight, const float* bias, const void* grad_out, void* grad_x,
-                    float* grad_weight, float* grad_bias, void* ws, cudaStream_t s);
+                    float* grad_weight, float* grad_bias, void* ws, int* err, cudaStream_t s);
 
 }  // namespace norm
 }  // namespace etp

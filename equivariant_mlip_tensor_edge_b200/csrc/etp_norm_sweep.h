@@ -531,7 +531,6 @@ __global__ void __launch_bounds__(kBlock, 1) k_norm(const __grid_constant__ Args
     if (lane == 0) {
       tc::mbar_init(&sh.gate, kWarps);
       sh.abort = 0;
-      if (blockIdx.x == 0) *p.err = 0;
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     __syncwarp();

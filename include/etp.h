@@ -307,6 +307,14 @@ etp_status etp_checkpoint_restore(etp_ckpt_format format, etp_dtype dtype, long 
  * 0 for shapes that are not supported. */
 size_t etp_group_norm_workspace_bytes(int lmax, int channels, int groups, int n_structs, int backward);
 
+/* Pipeline status of the group norm's calls, forward and backward, which have no handle: one sticky word
+ * for the process, 64 bytes of pinned host memory that the first call makes. A kernel that gives up a
+ * bounded wait leaves its outputs incomplete and its code here; from then on every call returns
+ * ETP_ERR_CUDA until etp_group_norm_status, like etp_get_status, has read and cleared it. The word's host
+ * address, for callers that poll it: etp_group_norm_status_word (NULL if it could not be made). */
+etp_status etp_group_norm_status(void* stream, int* code);
+int* etp_group_norm_status_word(void);
+
 /* Group norm with an activation on node rows x[n_nodes][dim], dim = channels (lmax + 1)^2, in the
  * uniform layout. Structure s is the rows node_ptr[s] .. node_ptr[s+1] - 1 (node_ptr: [n_structs + 1]
  * device ints, ascending, within [0, n_nodes]; NULL with n_structs = 1: all rows); group g is the
@@ -327,8 +335,8 @@ size_t etp_group_norm_workspace_bytes(int lmax, int channels, int groups, int n_
  * statistics' sums are taken in 64 bits (a row's squares of l > 0 in 32), the backward's in 32 within
  * a thread block and 64 between blocks; equal calls give equal bits. Asynchronous
  * (a cooperative launch); concurrent calls need a workspace each, 256-byte aligned. With ETP_VALIDATE=1
- * node_ptr is checked first (ETP_ERR_BAD_GRAPH), and the call waits and returns ETP_ERR_CUDA if a
- * bounded pipeline wait gave up. */
+ * node_ptr is checked first (ETP_ERR_BAD_GRAPH), and the call waits and returns ETP_ERR_CUDA if its
+ * kernel gave up a bounded wait; else later calls do (etp_group_norm_status). */
 etp_status etp_group_norm(int lmax, int channels, int groups, int n_nodes, int n_structs, const int* node_ptr,
                           etp_dtype dtype, const void* x, const float* weight, const float* bias, float eps,
                           etp_activation activation, int zero_rest, void* out, float* stats, etp_ckpt_format format,

@@ -4,6 +4,7 @@ import ctypes
 import os
 import shutil
 import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -185,3 +186,76 @@ def test_deviation_of_a_long_structure():
     bound = norm_bounds(_np(row), None, None, 1, groups, [0, 1], "silu", st, 0)
     for r in (0, n // 2, n - 1):
         _within(_np(out[r:r + 1]), want, bound, "out")
+
+
+# ------------------------------------------------------------------ waits that give up
+
+def test_status_word_gates_the_norm_until_it_is_read():
+    """A kernel that gives up a bounded wait stores its code in the status word of the norm's calls, and every
+    later one returns ETP_ERR_CUDA before any CUDA work. Here the test writes the word itself."""
+    lib, fake, other = etp.load_library(), ctypes.c_void_p(4096), ctypes.c_void_p(1 << 20)
+    word = lib.etp_group_norm_status_word()
+    assert word and word[0] == 0
+
+    def fwd(x=fake):
+        return lib.etp_group_norm(1, 8, 2, 4, 1, None, 0, x, None, None, 1e-5, 1, 0, other, fake, 0, None, None, fake, 1 << 30, None)
+
+    def bwd():
+        return lib.etp_group_norm_backward(1, 8, 2, 4, 1, None, 0, fake, 0, None, None, fake, None, None, 1, fake, 0, other,
+                                           None, None, fake, 1 << 30, None)
+    code = ctypes.c_int(-1)
+    try:
+        word[0] = 2
+        assert fwd() == 5 and "code 2" in lib.etp_last_error().decode()
+        assert bwd() == 5 and "code 2" in lib.etp_last_error().decode()
+        assert fwd(x=None) == 1          # arguments are checked first
+        assert lib.etp_group_norm_status(None, ctypes.byref(code)) == 5 and code.value == 2 and word[0] == 0
+        assert lib.etp_group_norm_status(None, ctypes.byref(code)) == 0 and code.value == 0
+        word[0] = 3
+        with pytest.raises(etp.EtpError) as e:
+            etp.group_norm_check_status()
+        assert e.value.status == 5 and "code 3" in str(e.value)
+        etp.group_norm_check_status()
+    finally:
+        word[0] = 0
+
+
+@pytest.mark.gpu
+def test_status_word_on_the_device(monkeypatch):
+    """Calls leave the word alone; a code in it stops the binding's calls until it is read."""
+    x = torch.randn(40, 32, device=DEV)
+    word = etp.load_library().etp_group_norm_status_word()
+    want = etp.group_norm(x, None, None, 1, 2)[0]
+    etp.group_norm_check_status(torch.device(DEV))
+    try:
+        word[0] = 1
+        for call in (lambda: etp.group_norm(x, None, None, 1, 2),
+                     lambda: etp.group_norm_backward(x, torch.zeros(1, 3, 2, device=DEV), None, None, x, 1, 2)):
+            with pytest.raises(etp.EtpError) as e:
+                call()
+            assert e.value.status == 5
+        with pytest.raises(etp.EtpError):
+            etp.group_norm_check_status(torch.device(DEV))
+    finally:
+        word[0] = 0
+    monkeypatch.setenv("ETP_VALIDATE", "1")
+    assert torch.equal(etp.group_norm(x, None, None, 1, 2)[0], want)
+
+
+@pytest.mark.gpu
+def test_first_call_of_a_process_may_be_captured():
+    """The word is made by the first call, also one that a stream captures."""
+    program = (
+        "import torch, equivariant_mlip_tensor_edge_b200 as etp\n"
+        "x = torch.randn(40, 32, device='cuda')\n"
+        "torch.cuda.synchronize()\n"
+        "graph = torch.cuda.CUDAGraph()\n"
+        "with torch.cuda.graph(graph):\n"
+        "    y = etp.group_norm(x, None, None, 1, 2)[0]\n"
+        "graph.replay()\n"
+        "torch.cuda.synchronize()\n"
+        "etp.group_norm_check_status(x.device)\n"
+        "assert torch.equal(y, etp.group_norm(x, None, None, 1, 2)[0])\n"
+        "print('captured')\n")
+    run = subprocess.run([sys.executable, "-c", program], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert run.returncode == 0 and "captured" in run.stdout, run.stderr[-2000:]
