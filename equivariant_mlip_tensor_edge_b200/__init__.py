@@ -690,18 +690,18 @@ def group_norm_function(checkpoint=None):
             out, stats, ck = group_norm(x.detach(), None if weight is None else weight.detach(),
                                         None if bias is None else bias.detach(), lmax, groups, node_ptr, eps, activation,
                                         checkpoint)
-            ctx.args = (lmax, groups, node_ptr, activation)
+            ctx.args = (lmax, groups, activation)
             ctx.kept_dtype = ck.dtype if ck else None
-            ctx.save_for_backward(*((ck.q, ck.scale) if ck else (x, None)), stats, weight, bias)
+            ctx.save_for_backward(*((ck.q, ck.scale) if ck else (x, None)), stats, weight, bias, node_ptr)
             return out
 
         @staticmethod
         @torch.autograd.function.once_differentiable
         def backward(ctx, grad_out):
-            x, scale, stats, weight, bias = ctx.saved_tensors
+            x, scale, stats, weight, bias, node_ptr = ctx.saved_tensors
             if ctx.kept_dtype is not None:
                 x = Checkpoint8(x, scale, ctx.kept_dtype)
-            lmax, groups, node_ptr, activation = ctx.args
+            lmax, groups, activation = ctx.args
             need = ctx.needs_input_grad
             gx, gw, gb = group_norm_backward(x, stats, weight, bias, grad_out, lmax, groups, node_ptr, activation,
                                              need[0], need[1] or need[2])

@@ -259,3 +259,22 @@ def test_first_call_of_a_process_may_be_captured():
         "print('captured')\n")
     run = subprocess.run([sys.executable, "-c", program], cwd=ROOT, capture_output=True, text=True, timeout=300)
     assert run.returncode == 0 and "captured" in run.stdout, run.stderr[-2000:]
+
+
+# ------------------------------------------------------------------ buffers that a program uses again
+
+@pytest.mark.gpu
+def test_node_ptr_changed_before_the_backward_is_refused():
+    """A batch's node_ptr overwritten for the next one would give wrong gradients: autograd says so, as it
+    does for x and the weights."""
+    x = torch.randn(20, 32, device=DEV, requires_grad=True)
+    w = torch.ones(2, 8, device=DEV, requires_grad=True)
+    for change in (0, 1):
+        ptr = torch.tensor([0, 12, 20], dtype=torch.int32, device=DEV)
+        y = etp.group_norm_function().apply(x, w, None, 1, 2, ptr)
+        if change:
+            ptr.copy_(torch.tensor([0, 4, 20], dtype=torch.int32))
+            with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+                y.sum().backward()
+        else:
+            y.sum().backward()
