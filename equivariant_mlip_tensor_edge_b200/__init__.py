@@ -585,6 +585,8 @@ def _norm_workspace(lmax, c, groups, s, backward, x, workspace):
         workspace = x.new_empty(max(nb, 1), dtype=_torch().uint8)
     elif workspace.get_device() != x.get_device():
         raise ValueError(f"workspace on {workspace.device}, tensors on {x.device}")
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
     return workspace, nb
 
 

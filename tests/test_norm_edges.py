@@ -278,3 +278,15 @@ def test_node_ptr_changed_before_the_backward_is_refused():
                 y.sum().backward()
         else:
             y.sum().backward()
+
+
+def test_workspace_with_strides_is_refused(monkeypatch):
+    """An expanded or strided workspace has fewer bytes behind its address than elements."""
+    monkeypatch.setattr(etp, "_one_device", lambda *tensors: 0)
+    monkeypatch.setattr(etp, "_call", lambda index, where, *args: pytest.fail(f"{where} was called"))
+    x, stats = torch.zeros(4, 32), torch.zeros(1, 3, 2)
+    for ws in (torch.empty(1, dtype=torch.uint8).expand(1 << 22), torch.empty(1 << 22, 2, dtype=torch.uint8)[:, 0]):
+        for call in (lambda: etp.group_norm(x, None, None, 1, 2, workspace=ws),
+                     lambda: etp.group_norm_backward(x, stats, None, None, x, 1, 2, workspace=ws)):
+            with pytest.raises(ValueError, match="contiguous"):
+                call()
