@@ -1012,10 +1012,10 @@ etp_status etp_group_norm(int lmax, int channels, int groups, int n_nodes, int n
   const StatusWord* word = nullptr;
   if ((st = norm_gate(who, &word)) != ETP_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (validate_requested() && (st = norm::validate(c, workspace, s)) != ETP_OK) return st;
   if (n_nodes == 0)
     return n_structs == 0 ? ETP_OK
                           : cuda_status(cudaMemsetAsync(stats, 0, sizeof(float) * n_structs * (lmax + 2) * groups, s), who);
-  if (validate_requested() && (st = norm::validate(c, workspace, s)) != ETP_OK) return st;
   st = norm::forward(c, x, weight, bias, eps, out, stats, format, static_cast<uint8_t*>(q),
                      static_cast<uint8_t*>(scale), workspace, word->dev, s);
   return st == ETP_OK ? norm_finished(who, s) : st;
@@ -1049,12 +1049,12 @@ etp_status etp_group_norm_backward(int lmax, int channels, int groups, int n_nod
   const StatusWord* word = nullptr;
   if ((st = norm_gate(who, &word)) != ETP_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (validate_requested() && (st = norm::validate(c, workspace, s)) != ETP_OK) return st;
   if (n_nodes == 0) {
     cudaError_t e = grad_weight ? cudaMemsetAsync(grad_weight, 0, sizeof(float) * (lmax + 1) * channels, s) : cudaSuccess;
     if (e == cudaSuccess && grad_bias) e = cudaMemsetAsync(grad_bias, 0, sizeof(float) * channels, s);
     return cuda_status(e, who);
   }
-  if (validate_requested() && (st = norm::validate(c, workspace, s)) != ETP_OK) return st;
   st = norm::backward(c, x, format, static_cast<const uint8_t*>(q), static_cast<const uint8_t*>(scale), stats, weight,
                       bias, grad_out, grad_x, grad_weight, grad_bias, workspace, word->dev, s);
   return st == ETP_OK ? norm_finished(who, s) : st;

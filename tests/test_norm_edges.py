@@ -290,3 +290,17 @@ def test_workspace_with_strides_is_refused(monkeypatch):
                      lambda: etp.group_norm_backward(x, stats, None, None, x, 1, 2, workspace=ws)):
             with pytest.raises(ValueError, match="contiguous"):
                 call()
+
+
+@pytest.mark.gpu
+def test_bad_node_ptr_of_no_rows(monkeypatch):
+    none, w = torch.empty(0, 32, device=DEV), torch.ones(2, 8, device=DEV)
+    monkeypatch.setenv("ETP_VALIDATE", "1")
+    bad, good = (torch.tensor(p, dtype=torch.int32, device=DEV) for p in ([0, 5], [0, 0]))
+    stats = etp.group_norm(none, w, None, 1, 2, good)[1]
+    etp.group_norm_backward(none, stats, w, None, none, 1, 2, good)
+    for call in (lambda: etp.group_norm(none, w, None, 1, 2, bad),
+                 lambda: etp.group_norm_backward(none, stats, w, None, none, 1, 2, bad)):
+        with pytest.raises(etp.EtpError) as e:
+            call()
+        assert e.value.status == 4
