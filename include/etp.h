@@ -331,7 +331,9 @@ int* etp_group_norm_status_word(void);
  * they were in out, or zeroed if zero_rest is nonzero. format: ETP_CKPT_NONE, or the checkpoint of all
  * rows of x is stored to q and scale as by etp_checkpoint_store (q 16-byte aligned), in the same
  * pass when channels % 32 == 0. lmax 0..3; channels / groups whole, groups <= 64, dim <= 4096, channels
- * <= 1024, 512 or 256 as channels / groups is a multiple of 4, of 2 or odd; eps >= 0. The
+ * <= 1024, 512 or 256 as channels / groups is a multiple of 4, of 2 or odd; eps >= 0.
+ * Values are squared in 32 bits: finite |x| up to 2^60 (squares of larger ones may overflow, which makes
+ * r_l 0, as for an infinity), and where eps is below 2^-120 deviations from 2^-60 on. The
  * statistics' sums are taken in 64 bits (a row's squares of l > 0 in 32), the backward's in 32 within
  * a thread block and 64 between blocks; equal calls give equal bits. Asynchronous
  * (a cooperative launch); concurrent calls need a workspace each, 256-byte aligned. With ETP_VALIDATE=1

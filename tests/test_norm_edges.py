@@ -304,3 +304,27 @@ def test_bad_node_ptr_of_no_rows(monkeypatch):
         with pytest.raises(etp.EtpError) as e:
             call()
         assert e.value.status == 4
+
+
+# ------------------------------------------------------------------ range
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("keep", [None, "int8", "e4m3"])
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("power,eps", [(57, 1e-5), (57, 0.0), (-57, 0.0)])
+def test_values_of_the_stated_range(power, eps, dtype, keep):
+    """Values around 2^57, up to 2^60, and deviations around 2^-57 without eps."""
+    n, lmax, c, groups = 300, 2, 32, 4
+    x, w, b, g = _norm_inputs(n, lmax, c, dtype, 31)
+    x = (x.clamp(-8, 8).float() * 2.0 ** power).to(x.dtype)
+    ptr = _starts("ragged", n)
+    xd, wd, bd = x.to(DEV), torch.from_numpy(w).to(DEV), torch.from_numpy(b).to(DEV)
+    node_ptr = torch.tensor(ptr, dtype=torch.int32, device=DEV)
+    out, stats, ck = etp.group_norm(xd, wd, bd, lmax, groups, node_ptr, eps=eps, checkpoint=keep)
+    want, st = norm64(_np(x), w, b, lmax, groups, ptr, eps, "silu")
+    info = torch.finfo(TYPES[dtype])
+    half = info.eps if dtype != "float32" else 0
+    _within(_np(stats)[:, 1:], st[:, 1:], 16 * 2.0 ** -24 * st[:, 1:], "deviation")
+    _within(_np(out), want, norm_bounds(_np(x), w, b, lmax, groups, ptr, "silu", st, half, tiny=info.smallest_normal), "out")
+    got = etp.group_norm_backward(ck if keep else xd, stats, wd, bd, g.to(DEV), lmax, groups, node_ptr)
+    _check_backward(keep64(_np(x), keep)[0] if keep else _np(x), w, b, g, lmax, groups, ptr, "silu", stats, got, dtype)
