@@ -412,15 +412,16 @@ def node_ladder_full(A, Ws, lmax, out=None, workspace=None):
 CKPT_FORMATS = {None: 0, "none": 0, "int8": 1, "e4m3": 2}
 ACTIVATIONS = {None: 0, "none": 0, "silu": 1}
 CKPT_BLOCK = 32   # values of a row that share a checkpoint scale
-_DTYPE_CODES = {}
+
+
+@functools.lru_cache(maxsize=None)
+def _dtype_codes():
+    torch = _torch()
+    return {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 
 
 def _dtype_code(dtype):
-    code = _DTYPE_CODES.get(dtype)
-    if code is None and not _DTYPE_CODES:
-        torch = _torch()
-        _DTYPE_CODES.update({torch.float32: 0, torch.bfloat16: 1, torch.float16: 2})
-        code = _DTYPE_CODES.get(dtype)
+    code = _dtype_codes().get(dtype)
     if code is None:
         raise ValueError(f"float32, bfloat16 or float16 values expected, got {dtype}")
     return code

@@ -1,6 +1,7 @@
 """Group norm and 8-bit checkpoints where sizes, ranges and arguments end: the launch plan replayed on the
 CPU, refusals, and kernels against float64 on the GPU."""
 import ctypes
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -328,3 +329,31 @@ def test_values_of_the_stated_range(power, eps, dtype, keep):
     _within(_np(out), want, norm_bounds(_np(x), w, b, lmax, groups, ptr, "silu", st, half, tiny=info.smallest_normal), "out")
     got = etp.group_norm_backward(ck if keep else xd, stats, wd, bd, g.to(DEV), lmax, groups, node_ptr)
     _check_backward(keep64(_np(x), keep)[0] if keep else _np(x), w, b, g, lmax, groups, ptr, "silu", stats, got, dtype)
+
+
+# ------------------------------------------------------------------ first calls at once
+
+def test_first_calls_of_two_threads():
+    """A thread's first call may come between any two lines of another's."""
+    for line in range(1, 9):
+        spec = importlib.util.spec_from_file_location("etp_again", etp.__file__)
+        again = importlib.util.module_from_spec(spec)
+        sys.modules["etp_again"] = again
+        seen = [0]
+
+        def other(frame, event, arg):
+            if frame.f_code.co_name != "_dtype_code":
+                return None
+            if event == "line":
+                seen[0] += 1
+                if seen[0] == line:
+                    sys.settrace(None)
+                    assert again._dtype_code(torch.bfloat16) == 1
+            return other
+        try:
+            spec.loader.exec_module(again)
+            sys.settrace(other)
+            assert again._dtype_code(torch.float32) == 0
+        finally:
+            sys.settrace(None)
+            del sys.modules["etp_again"]
