@@ -111,9 +111,15 @@ etp_status backward(const Call& c, const void* x, etp_ckpt_format format, const 
   p.part = reinterpret_cast<double*>(at);
   p.table = reinterpret_cast<float*>(at += partial_bytes(c));
   p.chan = reinterpret_cast<float*>(at + mean_bytes(c));
-  // Of 32-bit rows the backward takes two channels a thread: a row is in work for half as long, and more
-  // of the ring is under way (8 cells of 1000 atoms, 128 channels, rank 3, int8: 46 us, with four 58 us).
-  // 16-bit rows, half as long, do not gain (a training step of 12289 rows of 864: 75 us, with four 72).
+  // Of 32-bit rows the backward takes two channels a thread, of 16-bit rows four. Two keep a row in work for
+  // half as long and the sums in registers; four share a row's addresses, scales and codes among more
+  // values, but at rank 3 from a checkpoint they spill (240 to 300 bytes). Two / four channels, us, 8
+  // structures, 128 channels, 65.5 MB of float32 rows (or their values in bfloat16), from rows, int8, e4m3:
+  //            float32                               bfloat16
+  //   rank 1   52.0/52.1  45.4/42.9  45.5/41.7       36.6/33.0  43.0/37.0  43.1/36.2
+  //   rank 2   53.3/55.0  42.0/42.0  42.0/41.6       32.4/30.6  37.5/34.7  37.6/33.8
+  //   rank 3   53.6/56.4  43.3/48.3  43.1/47.5       31.5/31.0  36.2/41.3  36.3/39.6
+  // The type alone is not the best rule for rank 1 in 32 bits and rank 3 in 16 bits from checkpoints.
   int width = vector_width(c.channels, c.groups);
   if (c.dtype == ETP_F32 && width == 4 && c.channels / 2 <= kMaxVectors) width = 2;
   return launch_backward(c, p, kept, width, s);

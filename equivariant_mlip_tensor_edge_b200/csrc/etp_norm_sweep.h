@@ -20,10 +20,10 @@
 // rows fit on the chip) is not read again, and what comes next was read last and is likely in L2. A
 // structure that crosses blocks (two at most for a block: one that reaches in from before, one that goes
 // on behind) leaves partial sums, which meet after the grid barrier between the sweeps. The forward keeps
-// its sums in 64 bits, but for a row's squares of l > 0. The backward adds in 32 bits within a block, a
-// thread's rows and then the threads (joining the threads in 64 bits took the backward of 4000 structures
-// from 24.4 to 25.9 us), and in 64 from block to block. Every sum has one order, so equal calls give equal
-// bits.
+// its sums in 64 bits, but for a row's squares of l > 0 and a thread's sum of them as it is passed on. The
+// backward adds in 32 bits within a block, a thread's rows and then the threads (joining the threads in 64
+// bits took the backward of 4000 structures from 24.4 to 25.9 us), and in 64 from block to block. Every
+// sum has one order, so equal calls give equal bits.
 //
 // A thread holds V neighbouring channels (V = 4, 2 or 1, as the group size divides by it) of every rp-th
 // row and walks the row's components, so a channel's gate stays in its thread. Sums stay in
@@ -31,11 +31,13 @@
 // warps meet to add them up once for the rows that the ring holds, not at every structure's end.
 //
 // Measured on one B200 (148 SMs, 6449 GB/s copy rate), times of the kernel alone: 32768 rows of 9 x 128
-// float32, one structure, forward: 75 us for 302 MB read and written once, 62 % of the copy rate; 325 MB
-// cross DRAM (the ring and L2 spare 71 of the second sweep's 151 MB). 8 structures of 1000 rows of 16 x
-// 128 float32, backward from int8: 44 us, 53 %. Small calls are bound by the chain launch - first tile -
-// sums - grid barrier - outputs: 21 rows 6.7 us, 1000 rows of 576 backward 12.2 us. Between, by the warps'
-// dependent instructions (15 warps an SM; twice as many with half the registers were 5 to 20 % slower).
+// float32, one structure, forward: 75 us for 302 MB read and written once, 62 % of the copy rate. In a
+// chain of calls 381 MB cross DRAM: 230 read (the ring and L2 spare 72 of the second sweep's 151 MB), 151
+// written, part of it during the next call. 8 structures of 1000 rows of 16 x 128 float32, backward from
+// int8: 44 us, 53 %. Small calls are bound by the chain launch - first tile - sums - grid barrier -
+// outputs: 21 rows 6.7 us, 1000 rows of 576 backward 12.3 us. Between, by the warps' dependent
+// instructions: 15 warps an SM issue in 26 to 47 % of the cycles (twice as many with half the registers were
+// 5 to 24 % slower).
 #pragma once
 
 #include <cooperative_groups.h>

@@ -334,8 +334,8 @@ int* etp_group_norm_status_word(void);
  * <= 1024, 512 or 256 as channels / groups is a multiple of 4, of 2 or odd; eps >= 0.
  * Values are squared in 32 bits: finite |x| up to 2^60 (squares of larger ones may overflow, which makes
  * r_l 0, as for an infinity), and where eps is below 2^-120 deviations from 2^-60 on. The
- * statistics' sums are taken in 64 bits (a row's squares of l > 0 in 32), the backward's in 32 within
- * a thread block and 64 between blocks; equal calls give equal bits. Asynchronous
+ * statistics' sums are taken in 64 bits (in 32 a thread's squares of l > 0 within a row, and their sum
+ * once over its rows), the backward's in 32 within a thread block and 64 between blocks; equal calls give equal bits. Asynchronous
  * (a cooperative launch); concurrent calls need a workspace each, 256-byte aligned. With ETP_VALIDATE=1
  * node_ptr is checked first (ETP_ERR_BAD_GRAPH), and the call waits and returns ETP_ERR_CUDA if its
  * kernel gave up a bounded wait; else later calls do (etp_group_norm_status). */
@@ -347,7 +347,8 @@ etp_status etp_group_norm(int lmax, int channels, int groups, int n_nodes, int n
 /* Vector-Jacobian product of etp_group_norm for the cotangent grad_out (dtype): grad_x (dtype), and
  * grad_weight[lmax + 1][channels], grad_bias[channels] (float32, sums over all structures). Any may be
  * NULL, not all three (with n_nodes = 0, where grad_x has no values, also all). stats: from the forward. format ETP_CKPT_NONE: x is the forward's input;
- * otherwise x is ignored and the input is read from its checkpoint q, scale. Rows of no structure add
+ * otherwise x is ignored and the input is read from its checkpoint q, scale: code 2^(scale - 127) in 32
+ * bits, not held to dtype's range. Rows of no structure add
  * nothing; zero_rest as above, for grad_x. grad_x may not overlap grad_out or x.
  * x, grad_out, grad_x, q, scale: 16-byte aligned. */
 etp_status etp_group_norm_backward(int lmax, int channels, int groups, int n_nodes, int n_structs,

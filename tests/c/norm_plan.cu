@@ -71,7 +71,7 @@ int main() {
           const int l = c.lmax, dim = c.channels * (l + 1) * (l + 1);
           const int forward[kMaxStreams] = {dim * size, 0, 0}, rows_in[kMaxStreams] = {dim * size, dim * size, 0},
                     kept[kMaxStreams] = {dim * size, dim, (dim + 31) / 32};
-          replay(c, sh[3], 8 * (l + 2), forward, sms);
+          replay(c, sh[3], 16 + 4 * l, forward, sms);
           for (int width : {sh[3], std::min(sh[3], 2)}) {
             replay(c, width, 4 * (l + 2), rows_in, sms);
             replay(c, width, 4 * (l + 2), kept, sms);
