@@ -304,7 +304,7 @@ class EdgeConv:
 
     def backward(self, graph, x, W, grad_out, want_grad_x=True, want_grad_vec=True, grad_x=None,
                  grad_vec=None, workspace=None, path_mask=None):
-        """x: the forward's node features, or their Checkpoint8."""
+        """x: the forward's node features, or their Checkpoint8 (restored to float32 for the call)."""
         torch = _torch()
         _need_cuda(x.q if isinstance(x, Checkpoint8) else x, W, grad_out)
         x, W, grad_out = self._features(x), _f32(W), _f32(grad_out)
@@ -332,7 +332,8 @@ class EdgeConv:
 
     def backward_weights(self, graph, x, grad_out, grad_W=None, workspace=None):
         """dL/dW for L = <grad_out, forward(graph, x, W)>: [n_basis, n_paths, C], or [n_basis, cols] for
-        a general irreps handle. x: the forward's node features, or their Checkpoint8."""
+        a general irreps handle. x: the forward's node features, or their Checkpoint8 (restored to
+        float32 for the call)."""
         torch = _torch()
         _need_cuda(x.q if isinstance(x, Checkpoint8) else x, grad_out)
         x, grad_out = self._features(x), _f32(grad_out)
@@ -535,7 +536,7 @@ def _empty_checkpoint(x, fmt):
 def checkpoint8(x, fmt="int8"):
     """8-bit checkpoint of x [..., cols] (float32, bfloat16 or float16 CUDA tensor): a Checkpoint8.
 
-    fmt "int8": values within half a step of max|x| / 63.5 of their run of 32 at most; "e4m3": within
+    fmt "int8": values within half a step of max|x| / 63.5 of their run of 32 (or 2^-126) at most; "e4m3": within
     2^-4 of each value, or 2^-10 of the scale. EdgeConv.backward, EdgeConv.backward_weights and
     group_norm_backward take a Checkpoint8 in the place of x.
     """
@@ -718,8 +719,8 @@ def edge_conv_function(checkpoint=None):
     """torch.autograd.Function: out = conv(x, edge_vec, W); gradients for x, edge_vec and W.
 
     checkpoint "int8" or "e4m3": the node features are kept for the backward in 8 bits instead of
-    float32; the gradients for edge_vec and W are taken at the kept values (that for x does not depend
-    on x).
+    float32, and restored to a float32 copy by the backward; the gradients for edge_vec and W are taken at
+    the kept values (that for x does not depend on x).
     """
     torch = _torch()
     _named(CKPT_FORMATS, checkpoint, "checkpoint")

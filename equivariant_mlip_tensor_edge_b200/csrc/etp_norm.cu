@@ -113,7 +113,7 @@ etp_status backward(const Call& c, const void* x, etp_ckpt_format format, const 
   p.chan = reinterpret_cast<float*>(at + mean_bytes(c));
   // Of 32-bit rows the backward takes two channels a thread, of 16-bit rows four. Two keep a row in work for
   // half as long and the sums in registers; four share a row's addresses, scales and codes among more
-  // values, but at rank 3 from a checkpoint they spill (240 to 300 bytes). Two / four channels, us, 8
+  // values, but at rank 3 from a checkpoint they spill (272 to 304 bytes). Two / four channels, us, 8
   // structures, 128 channels, 65.5 MB of float32 rows (or their values in bfloat16), from rows, int8, e4m3:
   //            float32                               bfloat16
   //   rank 1   52.0/52.1  45.4/42.9  45.5/41.7       36.6/33.0  43.0/37.0  43.1/36.2

@@ -32,11 +32,11 @@
 //
 // Measured on one B200 (148 SMs, 6449 GB/s copy rate), times of the kernel alone: 32768 rows of 9 x 128
 // float32, one structure, forward: 75 us for 302 MB read and written once, 62 % of the copy rate. In a
-// chain of calls 381 MB cross DRAM: 230 read (the ring and L2 spare 72 of the second sweep's 151 MB), 151
+// chain of calls 382 MB cross DRAM: 231 read (the ring and L2 spare 71 of the second sweep's 151 MB), 151
 // written, part of it during the next call. 8 structures of 1000 rows of 16 x 128 float32, backward from
 // int8: 44 us, 53 %. Small calls are bound by the chain launch - first tile - sums - grid barrier -
 // outputs: 21 rows 6.7 us, 1000 rows of 576 backward 12.3 us. Between, by the warps' dependent
-// instructions: 15 warps an SM issue in 26 to 47 % of the cycles (twice as many with half the registers were
+// instructions: 15 warps an SM issue in 25 to 47 % of the cycles (twice as many with half the registers were
 // 5 to 24 % slower).
 #pragma once
 
