@@ -673,10 +673,10 @@ def group_norm_backward(x, stats, weight, bias, grad_out, lmax, groups, node_ptr
 
 
 def group_norm_check_status(device=None):
-    """Synchronise the current stream and raise if a kernel of an earlier group_norm or group_norm_backward
-    call gave up a bounded pipeline wait (the code is cleared). Until then later calls raise."""
+    """Synchronise the current stream (of ``device``) and raise if a kernel of an earlier group_norm or
+    group_norm_backward call gave up a bounded pipeline wait (the code is cleared). Until then later calls raise."""
     code = ctypes.c_int(0)
-    stream = _stream(device) if device is not None else None
+    stream = _stream(device) if _torch().cuda.is_available() else None
     _check(load_library().etp_group_norm_status(stream, ctypes.byref(code)), "etp_group_norm_status")
 
 
